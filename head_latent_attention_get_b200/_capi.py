@@ -26,6 +26,7 @@ MLA_ERR_DEVICE_BOUNDS = 6
 MLA_KV_BF16 = 0
 MLA_KV_FP8_E4M3 = 1
 MLA_KV_NVFP4 = 2
+MLA_KV_FP4_E2M1 = 3
 MLA_DEVICE_STATUS_TIMEOUT = 1
 MLA_DEVICE_STATUS_BOUNDS = 2
 MLA_DEBUG_WITHHOLD_SCORES = 1
@@ -33,6 +34,7 @@ MLA_DEBUG_SKIP_COMBINE = 2
 MLA_TILE_MD_INTS = 8
 MLA_MAX_ROWS = 128
 MLA_NOALLOC_WORKSPACE_BYTES = 48 << 20
+FP4_RECORD_BYTES = 416  # bytes of one MLA_KV_FP4_E2M1 token record
 
 
 class MLAError(RuntimeError):

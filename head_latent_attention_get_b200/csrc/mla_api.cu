@@ -81,7 +81,8 @@ mla_status_t check_common(const mla_decode_args* a, int topk) {
   if (a->batch <= 0 || a->s_q <= 0 || a->h_q <= 0 || a->h_kv <= 0 || a->num_pages <= 0 ||
       a->block_table_stride <= 0 || a->num_sm_parts <= 0)
     return MLA_ERR_INVALID_ARG;
-  if (a->kv_format != MLA_KV_BF16 && a->kv_format != MLA_KV_FP8_E4M3 && a->kv_format != MLA_KV_NVFP4)
+  if (a->kv_format != MLA_KV_BF16 && a->kv_format != MLA_KV_FP8_E4M3 && a->kv_format != MLA_KV_NVFP4 &&
+      a->kv_format != MLA_KV_FP4_E2M1)
     return MLA_ERR_INVALID_ARG;
   const bool nvfp4 = a->kv_format == MLA_KV_NVFP4;
   if (a->d_qk != (nvfp4 ? kNvfp4D : kDqk) || a->d_v != kDv || a->page_size != kPage) return MLA_ERR_INVALID_ARG;
@@ -106,14 +107,16 @@ mla_status_t run_decode(const mla_decode_args* a, const int32_t* indices, int to
   const int rows = g.rows;
   const int U = a->batch * g.units_per_req;
   const bool fp8 = a->kv_format == MLA_KV_FP8_E4M3;
-  const int mode = a->kv_format == MLA_KV_NVFP4 ? kModeNvfp4
+  const int mode = a->kv_format == MLA_KV_NVFP4      ? kModeNvfp4
+                   : a->kv_format == MLA_KV_FP4_E2M1 ? kModeFp4
                    : topk > 0                  ? (fp8 ? kModeFp8Sparse : kModeSparse)
                                                : (fp8 ? kModeFp8 : kModeBf16);
   // Q rows of every unit (not NVFP4: its query is dequantised by the kernel),
   // and (bf16 paged cache only) the cache as [pages*64 tokens][576 dims];
   // boxes of 64 x 64 with 128-B swizzle. The FP8 and NVFP4 paged modes copy
   // whole pages with cp.async.bulk, the sparse modes gather rows with
-  // cp.async: none of them needs a cache map.
+  // cp.async, 4-bit records are read by the converting threads: none of them
+  // needs a cache map.
   CUtensorMap tq, tkv, tv;
   std::memset(&tq, 0, sizeof(tq));
   std::memset(&tkv, 0, sizeof(tkv));
@@ -162,7 +165,9 @@ mla_status_t run_decode(const mla_decode_args* a, const int32_t* indices, int to
   p.kv_scale = static_cast<const uint8_t*>(a->kv_scale);
   const int rows_per_cta = rows < kRowsPerCta ? rows : kRowsPerCta;
   const cudaError_t e =
-      pair               ? launch_decode_pair(tq, tkv, tv, p, a->num_sm_parts, mode == kModeSparse, stream)
+      mode == kModeFp4   ? (row_groups == 2 ? launch_decode_fp4_pair(tq, p, a->num_sm_parts, topk > 0, stream)
+                                            : launch_decode_fp4(tq, p, a->num_sm_parts, topk > 0, stream))
+      : pair                           ? launch_decode_pair(tq, tkv, tv, p, a->num_sm_parts, mode == kModeSparse, stream)
       : (mode == kModeFp8 || mode == kModeNvfp4)
           ? launch_decode_page(mode, rows_per_cta, tq, p, a->num_sm_parts, row_groups, stream)
                          : launch_decode(rows_per_cta, mode, tq, tkv, tv, p, a->num_sm_parts, row_groups, stream);

@@ -17,6 +17,9 @@ constexpr int kFp8RecordBytes = 656;    // 512 e4m3 + 4 fp32 scales + 64 bf16
 constexpr int kNvfp4D = 512;            // NVFP4 rows: 512 values, K and V
 constexpr int kNvfp4RowBytes = 256;     // packed E2M1, two per byte
 constexpr int kNvfp4ScaleBytes = 32;    // one UE4M3 per 16 values
+constexpr int kFp4RecordBytes = 416;    // 256 B packed E2M1 + 32 UE4M3 scales + 64 bf16
+constexpr int kFp4ScaleOff = 256;
+constexpr int kFp4RopeOff = 288;
 constexpr size_t kWsHeaderBytes = 256;  // device status word lives at offset 0
 
 __host__ __device__ inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }

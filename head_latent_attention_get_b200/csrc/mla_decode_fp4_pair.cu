@@ -1,0 +1,472 @@
+// MLA decode over the 4-bit cache (MLA_KV_FP4_E2M1 records), units of 65-128
+// query rows, paged or token-sparse: one CTA pair (cluster of 2 CTAs on two
+// SMs) per scheduler part.
+//
+// Work split, TMEM layout and softmax are those of the bf16 pair kernel
+// (mla_decode_pair.cu): a step is two 128-token tiles; CTA r supplies K of
+// tile r and, for all 256 tokens, V of its value dims {256j + 128r + [0,128)}:
+//   S = Q K^T   pair MMA M=128 (64 rows per CTA) x N=256 tokens x K=576, bf16
+//   O = P V     pair MMA M=128 x N=256 value dims x K=256 tokens, twice, f16
+// Each CTA's eight converter warps fill its ring from the records
+// (mla_fp4.cuh) in the order in which the even CTA's MMA issuer consumes it.
+//
+// Warp roles (512 threads per CTA):
+//   0 Q via TMA (both CTAs; completion counted on the even CTA's barrier)
+//   1 TMEM allocation (both); MMA issue (even CTA); forwarding of the odd
+//     CTA's slot completions (odd CTA)
+//   2 cache rows   3 idle
+//   4-7 softmax + epilogue (both): thread i = (row i % 64, token half i / 64)
+//   8-15 converters
+// All waits are bounded; a timeout sets MLA_DEVICE_STATUS_TIMEOUT, raises the
+// abort flag of both CTAs, and every role winds down to the final cluster
+// barrier, which both CTAs always reach.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "mla_fp4.cuh"
+
+namespace mla {
+namespace fp4pair {
+
+constexpr int kN = 7;                // ring slots of 16 KB
+constexpr int kQBytes = 9 * 8192;    // 64 rows x 576 dims
+constexpr int kPBytes = 4 * 8192;    // 64 rows x 256 tokens (one buffer)
+constexpr int kTmemCols = 512;
+constexpr int kTmemS = 256;          // S buffers at columns 256 and 384; O at 0 and 128
+constexpr float kRescaleLog2 = 8.0f;
+
+struct Ctrl {
+  // barriers counted on the even CTA (the MMA issuer) ...
+  uint64_t q_full;                     // 1 arrival (+ both CTAs' Q bytes)
+  uint64_t full[kN];                   // 8 converter warps + 1 forward from the odd CTA
+  uint64_t p_full[2], o_free;          // 8 arrivals: 4 softmax warps x 2 CTAs
+  uint64_t drain;
+  // ... and in each CTA
+  uint64_t q_empty, empty[kN];         // pair-MMA commits
+  uint64_t s_full[2], o_done[2];       // pair-MMA commits; o_done[g & 1] completes O of step g
+  uint64_t v_loc[kN];                  // odd CTA: its 8 converter warps
+  uint64_t grp_sm;                     // 128 softmax threads
+  uint32_t tmem_base;
+  int abort_flag;
+  float mx[2][2][64];                  // [step parity][token half][row]: per-half tile max
+  float lx[2][64];                     // [token half][row]: per-half row sum
+};
+static_assert(sizeof(Ctrl) <= 2048, "control block");
+
+struct Smem {
+  static constexpr int q = 0;
+  static constexpr int ring = q + kQBytes;
+  static constexpr int pt = ring + kN * fp4::kSlot;
+  static constexpr int ctrl = pt + kPBytes;
+  static constexpr int rows = ctrl + 2048;
+  static constexpr int total = rows + (int)sizeof(fp4::RowTable);
+};
+static_assert(Smem::total + 1024 <= 232448, "shared memory budget");
+
+struct Pair {
+  uint32_t rank;
+  bool leader;
+  Ctrl* c;
+  uint32_t peer_abort;                 // cluster address of the other CTA's abort flag
+};
+
+__device__ __forceinline__ void raise_abort(const Pair& pr, const DecodeParams& p) {
+  atomicOr(p.status, (uint32_t)MLA_DEVICE_STATUS_TIMEOUT);
+  *(volatile int*)&pr.c->abort_flag = 1;
+  st_cluster_u32(pr.peer_abort, 1u);
+}
+
+__device__ __forceinline__ bool aborted(const Pair& pr) { return *(volatile int*)&pr.c->abort_flag != 0; }
+
+// Bounded wait with cluster-scope acquire (several barriers receive arrivals
+// from the other CTA or pair-MMA commits).
+__device__ __forceinline__ bool pwait(const Pair& pr, uint64_t* bar, uint32_t parity, const DecodeParams& p) {
+  if (aborted(pr)) return false;
+  if (mbar_wait_cluster(bar, parity, p.timeout_ns)) return true;
+  raise_abort(pr, p);
+  return false;
+}
+
+__device__ __forceinline__ bool group_sync(const Pair& pr, uint32_t& phase, const DecodeParams& p) {
+  mbar_arrive(&pr.c->grp_sm);
+  const bool ok = pwait(pr, &pr.c->grp_sm, phase & 1, p);
+  ++phase;
+  return ok;
+}
+
+// Arrive on barrier `bar` of the even CTA (a local arrive there, a remote one from the odd CTA).
+__device__ __forceinline__ void arrive_leader(const Pair& pr, uint64_t* bar) {
+  if (pr.leader) mbar_arrive(bar);
+  else mbar_arrive_cluster(map_to_rank(smem_u32(bar), 0));
+}
+
+template <bool SPARSE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
+    mla_decode_fp4_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const DecodeParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = smem + Smem::q;
+  uint8_t* sRing = smem + Smem::ring;
+  uint8_t* sP = smem + Smem::pt;
+  Ctrl* c = reinterpret_cast<Ctrl*>(smem + Smem::ctrl);
+  fp4::RowTable* rt = reinterpret_cast<fp4::RowTable*>(smem + Smem::rows);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  Pair pr;
+  pr.rank = cluster_rank();
+  pr.leader = pr.rank == 0;
+  pr.c = c;
+  pr.peer_abort = map_to_rank(smem_u32(&c->abort_flag), pr.rank ^ 1u);
+  const int part = blockIdx.x >> 1;
+  const int row0 = 64 * (int)pr.rank;   // first row of this CTA within a unit
+
+  if (threadIdx.x == 0) {
+    mbar_init(&c->q_full, 1);
+    for (int i = 0; i < kN; ++i) mbar_init(&c->full[i], fp4::kCvWarps + 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&c->p_full[i], 8);
+    mbar_init(&c->o_free, 8);
+    mbar_init(&c->drain, 1);
+    mbar_init(&c->q_empty, 1);
+    for (int i = 0; i < kN; ++i) mbar_init(&c->empty[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&c->s_full[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&c->o_done[i], 1);
+    for (int i = 0; i < kN; ++i) mbar_init(&c->v_loc[i], fp4::kCvWarps);
+    for (int i = 0; i < fp4::kRowDepth; ++i) {
+      mbar_init(&rt->full[i], 1);
+      mbar_init(&rt->empty[i], fp4::kCvWarps + (SPARSE ? 4 : 0));
+    }
+    mbar_init(&c->grp_sm, 128);
+    c->abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) tma_prefetch_desc(&tm_q);
+  if (warp == 1) {
+    tmem_alloc_pair(&c->tmem_base, kTmemCols);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync_all();  // barriers initialised and TMEM allocated in both CTAs
+  tc_fence_after();
+  const uint32_t tmem = c->tmem_base;
+  griddep_wait();  // the scheduler's output (and every input) is ready
+
+  PieceIter it;
+  it.init(p, part);
+  Piece pc;
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return pwait(pr, bar, parity, p); };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ Q
+    if (lane == 0) {
+      int pi = 0, q_issued = 0;
+      while (it.next(pc)) {
+        if (!pwait(pr, &c->q_empty, (pi & 1) ^ 1, p)) break;
+        const uint32_t qbar = map_to_rank(smem_u32(&c->q_full), 0);
+        if (pr.leader) mbar_arrive_expect_tx(&c->q_full, 2 * kQBytes);
+        const int qy = pc.unit * p.rows + row0;
+        for (int j = 0; j < 9; ++j) tma_load_2d_pair(sQ + j * 8192, &tm_q, qbar, 64 * j, qy);
+        ++q_issued;
+        ++pi;
+      }
+      // the even CTA's barrier counts both CTAs' copies
+      if (pr.leader && q_issued > 0) mbar_wait_cluster(&c->q_full, (uint32_t)((q_issued - 1) & 1), p.timeout_ns);
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    fp4::row_warp<true, SPARSE>(p, it, rt, lane, wait);
+  } else if (warp >= 8) {
+    fp4::convert_ring<true>(p, it, rt, sRing, c->empty, kN, warp - 8, lane, (int)pr.rank, wait,
+                            [&](int slot) { mbar_arrive(pr.leader ? &c->full[slot] : &c->v_loc[slot]); });
+  } else if (warp == 1 && !pr.leader) {
+    // ------------------------------------------------------------ odd CTA: forward slot completions
+    if (lane == 0) {
+      int sc = 0;
+      bool stop = false;
+      while (!stop && it.next(pc)) {
+        const int nslots = 17 * fp4::steps_of<true>(pc);  // 9 K and 8 V slots per step
+        for (int i = 0; i < nslots; ++i, ++sc) {
+          if (!pwait(pr, &c->v_loc[sc % kN], (sc / kN) & 1, p)) { stop = true; break; }
+          // relaxed: a release arrive would wait for memory operations that
+          // have nothing to do with the slot; the rows it signals are in
+          // shared memory (each converter fenced them before its arrival)
+          mbar_arrive_relaxed_cluster(map_to_rank(smem_u32(&c->full[sc % kN]), 0));
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer: S(0), S(1), O(0), S(2), O(1), ...
+    const uint32_t idesc_s = idesc_bf16(128, 256, false, false);
+    const uint32_t idesc_o = idesc_f16(128, 256, false, true);
+    int sc = 0, gs = 0, go = 0, pi = 0;
+    bool stop = false;
+    if (lane == 0) {
+      while (!stop && it.next(pc)) {
+        if (!pwait(pr, &c->q_full, pi & 1, p)) { stop = true; break; }
+        const int nsteps = fp4::steps_of<true>(pc);
+        for (int h = 0; h <= 2 * nsteps && !stop; ++h) {
+          if (!fp4::entry_exists(h, nsteps)) continue;
+          const int g = fp4::entry_step(h);
+          if (fp4::entry_is_k(h)) {
+            // S buffer b was last read by the softmax of step gs - 2, whose
+            // P the O product of step gs - 2 (issued just before) waited for
+            const int b = gs & 1;
+            tc_fence_after();
+            const uint32_t d = tmem + kTmemS + 128 * b;
+            for (int j = 0; j < 9; ++j, ++sc) {
+              const int slot = sc % kN;
+              if (!pwait(pr, &c->full[slot], (sc / kN) & 1, p)) { stop = true; break; }
+              tc_fence_after();
+              const uint32_t qa = smem_u32(sQ + j * 8192), kb = smem_u32(sRing + slot * fp4::kSlot);
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                mma_bf16_ss_pair(d, sdesc(qa + kk * 32, 16, 1024), sdesc(kb + kk * 32, 16, 1024), idesc_s,
+                                 (j | kk) != 0 ? 1u : 0u);
+              mma_commit_pair(&c->empty[slot]);
+            }
+            if (stop) break;
+            if (!(gs == 0 && (p.debug_flags & MLA_DEBUG_WITHHOLD_SCORES))) mma_commit_pair(&c->s_full[b]);
+            ++gs;
+            if (g == nsteps - 1) mma_commit_pair(&c->q_empty);  // Q is free once the last S completes
+          } else {
+            const bool first = g == 0;
+            if (first && pi > 0 && !pwait(pr, &c->o_free, (pi - 1) & 1, p)) { stop = true; break; }
+            if (!pwait(pr, &c->p_full[go & 1], (go >> 1) & 1, p)) { stop = true; break; }
+            const uint32_t pt = smem_u32(sP);
+            for (int q = 0; q < 4 && !stop; ++q) {
+              for (int jd = 0; jd < 2; ++jd, ++sc) {
+                const int slot = sc % kN;
+                if (!pwait(pr, &c->full[slot], (sc / kN) & 1, p)) { stop = true; break; }
+                tc_fence_after();
+                const uint32_t va = smem_u32(sRing + slot * fp4::kSlot);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                  mma_bf16_ss_pair(tmem + 128 * jd, sdesc(pt + q * 8192 + kk * 32, 16, 1024),
+                                   sdesc(va + kk * 2048, 8192, 1024), idesc_o, (first && q == 0 && kk == 0) ? 0u : 1u);
+                mma_commit_pair(&c->empty[slot]);
+              }
+            }
+            if (stop) break;
+            mma_commit_pair(&c->o_done[go & 1]);
+            ++go;
+          }
+        }
+        ++pi;
+      }
+      mma_commit_pair(&c->drain);  // every MMA this thread issued has completed before teardown
+      mbar_wait(&c->drain, 0, p.timeout_ns);
+    }
+    __syncwarp();
+  } else if (warp >= 4 && warp < 8) {
+    // ------------------------------------------------------------ softmax + epilogue
+    const int ti = threadIdx.x - 128;                     // TMEM lane of this thread
+    const int row = ti & 63, half = ti >> 6;
+    const int grow = row0 + row;                          // row within the unit
+    const bool rvalid = grow < p.rows;
+    const uint32_t lane_base = (uint32_t)(32 * (warp - 4)) << 16;
+    const float thresh = kRescaleLog2 / p.scale_log2;     // raw-score units
+    uint32_t gph = 0;
+    int gt = 0;
+    bool stop = false;
+    while (!stop && it.next(pc)) {
+      const int req = unit_req(p, pc.unit);
+      const int Ls = p.seqlens[req];
+      const int limit = p.causal ? Ls - p.s_q + row_query(p, pc.unit, grow) + 1 : Ls;
+      float m_used = -INFINITY, l_sum = 0.f;
+      int last_gt = -1;
+      for (int k = pc.t0; k < pc.t1 && !stop; k += 2, ++gt) {
+        const int b = gt & 1;
+        // validity of this thread's 128 keys: bit i of word w = key 32w + i
+        uint4 vm;
+        if (SPARSE) {
+          const int d = gt % fp4::kRowDepth;
+          if (!pwait(pr, &rt->full[d], (gt / fp4::kRowDepth) & 1, p)) { stop = true; break; }
+          vm = rvalid ? *reinterpret_cast<const uint4*>(&rt->valid[d][4 * half]) : make_uint4(0, 0, 0, 0);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&rt->empty[d]);
+        } else {
+          const int tile = k + half;
+          const int nv = (rvalid && tile < pc.t1) ? dense_tile_valid(limit, tile) : 0;
+          auto word = [nv](int w) {
+            const int nb = min(32, max(0, nv - 32 * w));
+            return nb >= 32 ? 0xffffffffu : ((1u << nb) - 1u);
+          };
+          vm = make_uint4(word(0), word(1), word(2), word(3));
+        }
+        if (!pwait(pr, &c->s_full[b], (gt >> 1) & 1, p)) { stop = true; break; }
+        tc_fence_after();
+        const uint32_t s_addr = tmem + lane_base + kTmemS + 128 * b;
+        // pass 1: max over this thread's 128 keys
+        float tmax = -INFINITY;
+#pragma unroll 1
+        for (int w = 0; w < 4; ++w) {
+          uint32_t sv[32];
+          tmem_ld32(s_addr + 32 * w, sv);
+          tmem_ld_wait();
+          const uint32_t mw = pick4u(vm, w);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) tmax = fmaxf(tmax, ((mw >> i) & 1u) ? __uint_as_float(sv[i]) : -INFINITY);
+        }
+        c->mx[gt & 1][half][row] = tmax;
+        if (!group_sync(pr, gph, p)) { stop = true; break; }
+        tmax = fmaxf(tmax, c->mx[gt & 1][half ^ 1][row]);
+        // both threads of a row take the same decision from the same values
+        float alpha = 1.f;
+        bool need = false;
+        if (tmax > m_used + thresh || (m_used == -INFINITY && tmax > -INFINITY)) {
+          alpha = (m_used == -INFINITY) ? 0.f : ex2_approx((m_used - tmax) * p.scale_log2);
+          need = (k != pc.t0) && (m_used != -INFINITY);
+          m_used = tmax;
+          l_sum *= alpha;
+        }
+        // pass 2: probabilities (masked by select) -> f16 -> the P buffer,
+        // K-major [64 rows][64 keys] per slice: keys 64s.. in slice s; this
+        // thread's keys are 128*half + [0,128), slices 2*half and 2*half + 1.
+        // The single P buffer was last read by the O product of step gt - 1,
+        // which must also be complete before O is rescaled. (O of step gt + 1,
+        // the next completion of the same barrier, needs this thread's P, so
+        // the parity wait never falls two phases behind.) The first
+        // quarter is computed into registers while that product runs.
+        const float mc = (m_used == -INFINITY ? 0.f : m_used) * p.scale_log2;
+        float part = 0.f;
+        auto probs = [&](int w, uint32_t (&pk)[16]) {
+          uint32_t sv[32];
+          tmem_ld32(s_addr + 32 * w, sv);
+          tmem_ld_wait();
+          const uint32_t mw = pick4u(vm, w);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float e0 = ex2_approx(fmaf(__uint_as_float(sv[2 * i]), p.scale_log2, -mc));
+            const float e1 = ex2_approx(fmaf(__uint_as_float(sv[2 * i + 1]), p.scale_log2, -mc));
+            const float p0 = ((mw >> (2 * i)) & 1u) ? e0 : 0.f;
+            const float p1 = ((mw >> (2 * i + 1)) & 1u) ? e1 : 0.f;
+            pk[i] = pack_f16x2(p0, p1);
+            part += p0 + p1;
+          }
+        };
+        auto store = [&](int w, const uint32_t (&pk)[16]) {
+          uint8_t* rowp = sP + (2 * half + (w >> 1)) * 8192 + (row >> 3) * 1024 + (row & 7) * 128;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int ch = 4 * (w & 1) + q;
+            *reinterpret_cast<uint4*>(rowp + ((ch ^ (row & 7)) << 4)) =
+                make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
+          }
+        };
+        uint32_t pk[16];
+        probs(0, pk);
+        if (gt >= 1 && !pwait(pr, &c->o_done[(gt - 1) & 1], ((gt - 1) >> 1) & 1, p)) { stop = true; break; }
+        store(0, pk);
+#pragma unroll 1
+        for (int w = 1; w < 4; ++w) {
+          probs(w, pk);
+          store(w, pk);
+        }
+        tc_fence_after();
+        l_sum += part;
+        if (need) {
+          // O holds every product up to step gt - 1 (waited for above)
+#pragma unroll 1
+          for (int c16 = 0; c16 < 16; ++c16) {  // 2 x 128 columns of this row
+            uint32_t ov[16];
+            const uint32_t a = tmem + lane_base + 16 * c16;
+            tmem_ld16(a, ov);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
+            tmem_st16(a, ov);
+          }
+          tmem_st_wait();
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_leader(pr, &c->p_full[b]);  // P written, O rescaled, scores consumed
+        last_gt = gt;
+      }
+      if (stop) break;
+      // ---------------- epilogue of the piece
+      c->lx[half][row] = l_sum;
+      if (!group_sync(pr, gph, p)) { stop = true; break; }
+      const float l_tot = l_sum + c->lx[half ^ 1][row];
+      if (last_gt >= 0 && !pwait(pr, &c->o_done[last_gt & 1], (last_gt >> 1) & 1, p)) { stop = true; break; }
+      tc_fence_after();
+      float inv = 0.f, lse = -INFINITY;
+      if (l_tot > 0.f) {
+        inv = 1.f / l_tot;
+        lse = m_used * p.scale + logf(l_tot);
+      }
+      if (pc.single && rvalid && p.sink != nullptr) inv *= fold_sink(lse, p.sink[row_head(p, pc.unit, grow)]);
+      const size_t orow = (size_t)pc.unit * p.rows + grow;
+      if (rvalid && half == 0) {
+        if (pc.single) p.lse[orow] = lse;
+        else p.ws_lse[(size_t)pc.ws_idx * p.rows + grow] = lse;
+      }
+#pragma unroll 1
+      for (int jd = 0; jd < 2; ++jd) {
+        const int d0 = 256 * jd + 128 * half;
+#pragma unroll 1
+        for (int c16 = 0; c16 < 8; ++c16) {
+          uint32_t ov[16];
+          tmem_ld16(tmem + lane_base + 128 * jd + 16 * c16, ov);
+          tmem_ld_wait();
+          if (rvalid) {
+            if (pc.single) {
+              uint32_t pk[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                pk[i] = pack_bf16x2(__uint_as_float(ov[2 * i]) * inv, __uint_as_float(ov[2 * i + 1]) * inv);
+              uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + orow * kDv + d0 + 16 * c16);
+              dst[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+              dst[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+            } else {
+              float4* dst = reinterpret_cast<float4*>(p.ws_o + ((size_t)pc.ws_idx * p.rows + grow) * kDv + d0 + 16 * c16);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                dst[i] = make_float4(__uint_as_float(ov[4 * i]) * inv, __uint_as_float(ov[4 * i + 1]) * inv,
+                                     __uint_as_float(ov[4 * i + 2]) * inv, __uint_as_float(ov[4 * i + 3]) * inv);
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_leader(pr, &c->o_free);
+    }
+  }
+
+  // ---------------------------------------------------------------- teardown
+  // In a normal exit every copy has landed: the MMA issuer consumed each Q
+  // phase, and the converters waited for their own copies. After an abort (a
+  // bounded wait ran out) a Q copy of the odd CTA may still be in flight, and
+  // its completion is counted on the even CTA's barrier, where no wait here
+  // observes it. Such copies land within microseconds, so the CTA holds its
+  // shared memory for a fixed 200 us of wall time (%globaltimer, not a sleep hint that may
+  // return early) before the final cluster barrier; this bounds the window,
+  // it does not prove every copy landed.
+  if (aborted(pr)) {
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < 200000) {
+    }
+  }
+  griddep_launch_dependents();  // the combine may be scheduled (it waits for this grid)
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // no pair MMA, copy or remote arrive of either CTA is still pending
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem, kTmemCols);
+}
+
+}  // namespace fp4pair
+
+cudaError_t launch_decode_fp4_pair(const CUtensorMap& tq, const DecodeParams& p, int parts, bool sparse,
+                                   cudaStream_t stream) {
+  constexpr int smem = fp4pair::Smem::total + 1024;
+  auto kern = sparse ? fp4pair::mla_decode_fp4_pair_kernel<true> : fp4pair::mla_decode_fp4_pair_kernel<false>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(kern, dim3(2 * parts), dim3(fp4::kThreads), smem, stream, tq, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace mla

@@ -1,0 +1,302 @@
+// Device code shared by the two decode kernels of the 4-bit cache
+// (mla_decode_fp4.cu, mla_decode_fp4_pair.cu): the order of the operand ring,
+// the warp that resolves cache rows, and the eight warps that turn 416-byte
+// token records into tensor-core operands.
+//
+// A record is 256 bytes of E2M1 pairs, 32 UE4M3 scales (one per 16 latent
+// values) and 64 bf16 RoPE dims. K takes bf16 (the query's type: one MMA wants
+// one type for both operands), V takes f16 (the probabilities are written in
+// f16 too). Both are exact: an E2M1 x UE4M3 product has at most 6 significant
+// bits and lies in [2^-10, 2688].
+//
+// Nothing raw is staged in shared memory. A converter thread keeps the codes
+// of the next eight slots in registers: slot i of a phase is converted, and
+// its register then takes slot i of the phase after it, so a load has a whole
+// phase (eight slots) to arrive. Reading the codes again for V costs 256 bytes
+// a token from L2, a quarter of what the bf16 cache's V re-read costs, and
+// leaves all shared memory beside Q and P to the ring.
+#pragma once
+#include <cuda_fp16.h>
+
+#include "mla_decode_util.cuh"
+
+namespace mla {
+namespace fp4 {
+
+constexpr int kSlot = 16384;     // a K slice (128 tokens x 64 dims) or a V slot (64 tokens x 128 dims, two halves)
+constexpr int kCvWarps = 8;
+constexpr int kRowDepth = 4;     // steps whose cache rows are resolved ahead
+constexpr int kThreads = 256 + 32 * kCvWarps;
+
+// Ring order of a piece of n steps: h = 0 -> K of step 0; h = 2g+1 -> K of
+// step g+1 (only if g+1 < n); h = 2g+2 -> V of step g. A K entry is nine
+// slots (eight latent slices, then RoPE), a V entry eight.
+__device__ __forceinline__ bool entry_exists(int h, int nsteps) { return !((h & 1) && (h >> 1) + 1 >= nsteps); }
+__device__ __forceinline__ bool entry_is_k(int h) { return h == 0 || (h & 1); }
+__device__ __forceinline__ int entry_step(int h) { return h == 0 ? 0 : (h & 1) ? (h >> 1) + 1 : (h >> 1) - 1; }
+
+// Steps of a piece: one 128-token tile (a single CTA) or two (a CTA pair).
+template <bool PAIR>
+__device__ __forceinline__ int steps_of(const Piece& pc) {
+  return PAIR ? (pc.t1 - pc.t0 + 1) >> 1 : pc.t1 - pc.t0;
+}
+
+// Walks the ring entries of every piece of a part.
+template <bool PAIR>
+struct Phases {
+  PieceIter it;
+  Piece pc;
+  int h = 0, nsteps = 0, step0 = 0;  // step0: index of the piece's first step among the part's steps
+  bool in_piece = false;
+  __device__ bool next() {
+    if (in_piece) {
+      do ++h;
+      while (h <= 2 * nsteps && !entry_exists(h, nsteps));
+      if (h <= 2 * nsteps) return true;
+      step0 += nsteps;
+    }
+    in_piece = it.next(pc);
+    if (!in_piece) return false;
+    nsteps = steps_of<PAIR>(pc);
+    h = 0;
+    return true;
+  }
+  __device__ bool is_k() const { return entry_is_k(h); }
+  __device__ int step() const { return step0 + entry_step(h); }
+};
+
+// Cache rows of the steps in flight (-1: past the request's end, outside the
+// piece or an ignored index: converted to zeros), and with token-sparse
+// indices the key validity bits (word w, bit i = key 32w + i of the step).
+struct RowTable {
+  uint64_t full[kRowDepth], empty[kRowDepth];
+  int32_t row[kRowDepth][256];
+  uint32_t valid[kRowDepth][8];
+};
+
+// 16 bytes that are read once per CTA and ring: no L1 line is kept for them.
+__device__ __forceinline__ uint4 ldg16(const uint8_t* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+// ---------------------------------------------------------------- conversions
+// Eight E2M1 codes (one word, element i in nibble i) -> 8 bf16 times a scale.
+// The magnitudes' bf16 high and low bytes come from byte permutes that use
+// the nibbles themselves as selectors; the sign bytes from permutes in their
+// sign-replicating form. (The hardware conversion gives f16, and f16 -> bf16
+// would cost three more instructions per pair.)
+__device__ __forceinline__ uint4 e2m1x8_to_bf16(uint32_t w, __nv_bfloat162 s) {
+  const uint32_t m = w & 0x77777777u, wl = w << 4;
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t sel = m >> (16 * i);
+    uint32_t sign, hi, lo;
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(sign) : "r"(wl), "r"(w), "r"(i == 0 ? 0xD9C8u : 0xFBEAu));
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(hi) : "r"(0x3F3F3F00u), "r"(0x40404040u), "r"(sel));
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(lo) : "r"(0xC0800000u), "r"(0xC0804000u), "r"(sel));
+    hi |= sign & 0x80808080u;
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(o[2 * i]) : "r"(lo), "r"(hi), "r"(0x5140u));
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(o[2 * i + 1]) : "r"(lo), "r"(hi), "r"(0x7362u));
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 v = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&o[i]), s);
+    o[i] = *reinterpret_cast<const uint32_t*>(&v);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+// The same in f16, by the hardware conversion of a byte into two f16.
+__device__ __forceinline__ uint4 e2m1x8_to_f16(uint32_t w, __half2 s) {
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2_raw hr = __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)((w >> (8 * i)) & 0xFFu), __NV_E2M1);
+    const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&hr), s);
+    o[i] = *reinterpret_cast<const uint32_t*>(&v);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+// Two UE4M3 scale bytes (bit 7 ignored) as f16.
+__device__ __forceinline__ __half2 ue4m3x2(uint32_t s) {
+  const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(s & 0x7F7Fu), __NV_E4M3);
+  return *reinterpret_cast<const __half2*>(&hr);
+}
+
+// 32 codes and their two scales.
+struct Item {
+  uint4 c;
+  uint32_t s;
+};
+__device__ __forceinline__ Item load_item(const uint8_t* cache, int row, int dim0) {
+  Item it;
+  it.c = make_uint4(0, 0, 0, 0);
+  it.s = 0;
+  if (row >= 0) {
+    const uint8_t* rec = cache + (size_t)row * kFp4RecordBytes;
+    it.c = ldg16(rec + dim0 / 2);
+    it.s = *reinterpret_cast<const uint16_t*>(rec + kFp4ScaleOff + dim0 / 16);
+  }
+  return it;
+}
+// Writes the item's 32 values as chunks c0..c0+3 of 128-byte row `row` of a swizzled tile.
+template <bool K>
+__device__ __forceinline__ void store_item(const Item& it, uint8_t* tile, int row, int c0) {
+  const __half2 sc = ue4m3x2(it.s);
+  const uint32_t w[4] = {it.c.x, it.c.y, it.c.z, it.c.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half s1 = i < 2 ? __low2half(sc) : __high2half(sc);
+    uint4 v;
+    if (K) v = e2m1x8_to_bf16(w[i], __bfloat162bfloat162(__float2bfloat16_rn(__half2float(s1))));
+    else v = e2m1x8_to_f16(w[i], __half2half2(s1));
+    *reinterpret_cast<uint4*>(sw128(tile, row, c0 + i)) = v;
+  }
+}
+
+// ---------------------------------------------------------------- row warp
+// One warp resolves the rows of every step of the part, up to kRowDepth steps
+// ahead of the slowest reader. `wait(bar, parity)` is the kernel's bounded wait.
+template <bool PAIR, bool SPARSE, class Wait>
+__device__ __forceinline__ void row_warp(const DecodeParams& p, PieceIter it, RowTable* rt, int lane, Wait wait) {
+  constexpr int kTok = PAIR ? 256 : 128;
+  Piece pc;
+  int gs = 0;
+  bool stop = false;
+  while (!stop && it.next(pc)) {
+    const int req = unit_req(p, pc.unit);
+    const int Ls = p.seqlens[req];
+    const int npg = (Ls + kPage - 1) / kPage;
+    const int n = steps_of<PAIR>(pc);
+    for (int g = 0; g < n; ++g, ++gs) {
+      const int d = gs % kRowDepth;
+      bool ok = true;
+      if (lane == 0) ok = wait(&rt->empty[d], ((gs / kRowDepth) & 1) ^ 1);
+      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      if (!ok) { stop = true; break; }
+      const int tok0 = (pc.t0 + (PAIR ? 2 : 1) * g) * kTile, end = min(pc.t1 * kTile, SPARSE ? p.topk : Ls);
+#pragma unroll
+      for (int w = 0; w < kTok / 32; ++w) {
+        const int t = tok0 + 32 * w + lane;
+        int row = -1;
+        if (t < end) {
+          if (SPARSE) row = sparse_row(p, pc.unit, t, true);
+          else row = page_of(p, req, t / kPage, npg) * kPage + t % kPage;
+        }
+        rt->row[d][32 * w + lane] = row;
+        if (SPARSE) {
+          const uint32_t m = __ballot_sync(0xffffffffu, row >= 0);
+          if (lane == 0) rt->valid[d][w] = m;
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&rt->full[d]);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- converters
+// Fills the ring, one item of 32 codes per thread and slot. K slot: thread
+// (token 16 cw + lane % 16, half lane / 16 of the slice's 64 dims); V slot:
+// thread (token 8 cw + lane % 8, quarter lane / 8 of the slot's 128 dims);
+// eight neighbouring lanes write the same chunk of eight rows, which the
+// swizzle spreads over all banks. The RoPE slice goes straight into its slot
+// with cp.async and is handed over after the next phase's second slot.
+// wait(bar, parity): the kernel's bounded wait; full(slot): one lane per warp
+// hands the slot over.
+template <bool PAIR, class Wait, class Full>
+__device__ __forceinline__ void convert_ring(const DecodeParams& p, const PieceIter& it, RowTable* rt, uint8_t* ring,
+                                             uint64_t* empty, int nslots, int cw, int lane, int rank, Wait wait,
+                                             Full full) {
+  const uint8_t* cache = static_cast<const uint8_t*>(p.kcache);
+  const int ktok = 16 * cw + (lane & 15), khalf = lane >> 4;
+  const int vtok = 8 * cw + (lane & 7), vq = lane >> 3;
+  auto load = [&](const Phases<PAIR>& ph, int i) {
+    const int32_t* rows = rt->row[ph.step() % kRowDepth];
+    if (ph.is_k()) return load_item(cache, rows[(PAIR ? 128 * rank : 0) + ktok], 64 * i + 32 * khalf);
+    // V slot i: a pair's (64-token quarter i / 2, value dims 256 (i % 2) + 128 rank ..),
+    // a single CTA's (value dims 128 (i / 2) .., 64-token half i % 2)
+    const int tq = PAIR ? i >> 1 : i & 1, d0 = PAIR ? 256 * (i & 1) + 128 * rank : 128 * (i >> 1);
+    return load_item(cache, rows[64 * tq + vtok], d0 + 32 * vq);
+  };
+  auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
+    bool ok = true;
+    if (lane == 0) ok = wait(bar, parity);
+    return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+  };
+  Phases<PAIR> nxt;  // the phase being loaded, one ahead of the phase being converted
+  nxt.it = it;
+  Item buf[8];
+  int slot = 0, rope_slot = -1;
+  uint32_t par = 1;  // parity to wait for on the slot's empty barrier
+  auto advance = [&] {
+    if (++slot == nslots) {
+      slot = 0;
+      par ^= 1;
+    }
+  };
+  auto retire_rope = [&] {
+    cp_async_wait<0>();
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) full(rope_slot);
+    rope_slot = -1;
+  };
+  bool have = nxt.next();
+  if (have) {
+    if (!wait_warp(&rt->full[0], 0)) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) buf[i] = load(nxt, i);
+  }
+  bool stop = false;
+  while (have && !stop) {
+    const bool k = nxt.is_k();
+    const int step = nxt.step();
+    have = nxt.next();
+    if (have && nxt.is_k()) {
+      const int s = nxt.step();
+      if (!wait_warp(&rt->full[s % kRowDepth], (s / kRowDepth) & 1)) break;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (!wait_warp(&empty[slot], par)) { stop = true; break; }
+      uint8_t* s = ring + slot * kSlot;
+      if (k) store_item<true>(buf[i], s, ktok, 4 * khalf);
+      else store_item<false>(buf[i], s + (vq >> 1) * 8192, vtok, 4 * (vq & 1));
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) full(slot);
+      advance();
+      if (have) buf[i] = load(nxt, i);
+      if (i == 1 && rope_slot >= 0) retire_rope();
+    }
+    if (stop) break;
+    if (k) {  // RoPE slice: 8 lanes per 128-byte row
+      if (!wait_warp(&empty[slot], par)) break;
+      const int32_t* rows = rt->row[step % kRowDepth] + (PAIR ? 128 * rank : 0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int t = 16 * cw + 4 * i + (lane >> 3), ch = lane & 7;
+        const int row = rows[t];
+        cp_async16(sw128(ring + slot * kSlot, t, ch),
+                   cache + (size_t)(row >= 0 ? row : 0) * kFp4RecordBytes + kFp4RopeOff + 16 * ch, row >= 0 ? 16u : 0u);
+      }
+      cp_async_commit();
+      rope_slot = slot;
+      advance();
+    }
+    // the rows of a step are last read by the loads of its V entry
+    if (have && !nxt.is_k()) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&rt->empty[nxt.step() % kRowDepth]);
+    }
+  }
+  cp_async_wait<0>();  // no copy may land after the CTA has finished
+}
+
+}  // namespace fp4
+}  // namespace mla

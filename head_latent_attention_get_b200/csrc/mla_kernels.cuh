@@ -8,8 +8,9 @@
 namespace mla {
 
 // Cache format x key-set kind: BF16 paged, FP8 paged, BF16 token-sparse,
-// FP8 token-sparse, NVFP4 paged (512-value rows, NVFP4 query).
-enum KvMode : int { kModeBf16 = 0, kModeFp8 = 1, kModeSparse = 2, kModeFp8Sparse = 3, kModeNvfp4 = 4 };
+// FP8 token-sparse, NVFP4 paged (512-value rows, NVFP4 query), 4-bit records
+// (paged or token-sparse).
+enum KvMode : int { kModeBf16 = 0, kModeFp8 = 1, kModeSparse = 2, kModeFp8Sparse = 3, kModeNvfp4 = 4, kModeFp4 = 5 };
 __host__ __device__ constexpr bool mode_fp8(int mode) { return mode == kModeFp8 || mode == kModeFp8Sparse; }
 __host__ __device__ constexpr bool mode_sparse(int mode) { return mode == kModeSparse || mode == kModeFp8Sparse; }
 
@@ -92,6 +93,12 @@ cudaError_t launch_decode_page(int mode, int rows_per_cta, const CUtensorMap& tq
 // CTA pairs (clusters of two), one per part.
 cudaError_t launch_decode_pair(const CUtensorMap& tq, const CUtensorMap& tkv, const CUtensorMap& tv,
                                const DecodeParams& p, int parts, bool sparse, cudaStream_t stream);
+// 4-bit records, paged or token-sparse: units of at most 64 rows, one CTA per
+// part, and of 65-128 rows, one CTA pair per part.
+cudaError_t launch_decode_fp4(const CUtensorMap& tq, const DecodeParams& p, int parts, bool sparse,
+                              cudaStream_t stream);
+cudaError_t launch_decode_fp4_pair(const CUtensorMap& tq, const DecodeParams& p, int parts, bool sparse,
+                                   cudaStream_t stream);
 // How many CTA pairs of the pair kernel can be resident at once on the current device (0 if unknown).
 int max_pair_clusters();
 // Unit u reads seqlens[u / upr] (paged decoding; upr = units per request);

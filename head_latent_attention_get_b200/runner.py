@@ -17,8 +17,8 @@ class DecodeRunner:
     def __init__(self, q, kcache, block_table, cache_seqlens, *, softmax_scale, causal=False,
                  indices=None, num_sm_parts=None, timeout_ns=0, debug_flags=0, sink=None, q_scale=None,
                  kv_scale=None):
-        """q bf16 [B, s_q, h_q, 576] with a bf16 or FP8-record cache, or (NVFP4)
-        packed uint8 [B, s_q, h_q, 256] with q_scale/kv_scale and a packed
+        """q bf16 [B, s_q, h_q, 576] with a bf16 cache or a cache of FP8 (656-byte)
+        or 4-bit (416-byte) records, or (NVFP4) packed uint8 [B, s_q, h_q, 256] with q_scale/kv_scale and a packed
         uint8 [pages, 64, 256] cache."""
         dev = q.device
         assert dev.type == "cuda", "the decode path runs on a CUDA device only"
@@ -29,7 +29,10 @@ class DecodeRunner:
             self.kv_format, d_qk = C.MLA_KV_NVFP4, 512
         else:
             assert d == 576
-            self.kv_format = C.MLA_KV_BF16 if kcache.dtype == torch.bfloat16 else C.MLA_KV_FP8_E4M3
+            if kcache.dtype == torch.bfloat16:
+                self.kv_format = C.MLA_KV_BF16
+            else:
+                self.kv_format = C.MLA_KV_FP4_E2M1 if kcache.shape[-1] == C.FP4_RECORD_BYTES else C.MLA_KV_FP8_E4M3
             d_qk = 576
         self.q_scale, self.kv_scale = q_scale, kv_scale
         upr, self.rows = C.mla_decode_geometry(self.s_q, self.h_q, 1, self.topk)

@@ -90,7 +90,16 @@ enum {
    * scales [batch, s_q, h_q, 32] in q_scale. value = e2m1 * ue4m3 (UE4M3:
    * E4M3 without a sign; bit 7 is ignored), exact in bf16, which the tensor
    * cores then use. Paged decoding only. */
-  MLA_KV_NVFP4 = 2
+  MLA_KV_NVFP4 = 2,
+  /* uint8 [num_pages, 64, 416] token records of 576-value rows, byte layout
+   *   [0,256)   512 latent values, packed E2M1 (element 2i in the low nibble
+   *             of byte i, 2i+1 in the high nibble)
+   *   [256,288) 32 UE4M3 scales, scale j applies to latent dims [16j, 16j+16)
+   *   [288,416) 64 bf16 RoPE dims
+   * value = e2m1 * ue4m3 (bit 7 of a scale byte is ignored), used exactly;
+   * the RoPE dims are used as stored. The query is bf16, 576 values. Paged
+   * and token-sparse decoding; the probabilities are rounded to f16. */
+  MLA_KV_FP4_E2M1 = 3
 };
 
 /* Bits of the device status word kept at the start of the workspace. */

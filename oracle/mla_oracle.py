@@ -168,6 +168,18 @@ def dequant_fp8_records(records) -> np.ndarray:
     return out
 
 
+FP4_RECORD_BYTES = 416
+
+
+def dequant_fp4_records(records) -> np.ndarray:
+    """uint8 [P, 64, 416] token records -> fp64 [P, 64, 576] rows: the latent
+    dims are the NVFP4 values of bytes [0, 256) (packed E2M1) and [256, 288)
+    (UE4M3 scales), the RoPE dims the bf16 of bytes [288, 416)."""
+    rec = np.ascontiguousarray(np.asarray(records, dtype=np.uint8))
+    rope_bits = rec[..., 288:].copy().view(np.uint16)
+    return np.concatenate([dequant_nvfp4(rec[..., :256], rec[..., 256:288]), bf16_bits_to_f64(rope_bits)], axis=-1)
+
+
 # --------------------------------------------------------------------------
 # the attention definition
 # --------------------------------------------------------------------------
@@ -308,6 +320,8 @@ def inputs_to_f64(inp):
     if inp.workload.kv == "nvfp4":
         return (dequant_nvfp4(inp.q.numpy(), inp.q_scale.numpy()),
                 dequant_nvfp4(inp.kcache.numpy(), inp.kv_scale.numpy()))
+    if inp.workload.kv == "fp4":
+        return torch_bf16_to_f64(inp.q), dequant_fp4_records(inp.kcache.numpy())
     return torch_bf16_to_f64(inp.q), cache_to_f64(inp.kcache)
 
 

@@ -13,6 +13,9 @@ one row per token serving as K (all 576 dims) and V (first 512 dims); pages of
   kcache fp8   [num_pages, 64, 656]      uint8 token records:
                  512 e4m3 latent codes | 4 fp32 scales (one per 128-element
                  tile, scale = amax/448) | 64 bf16 RoPE dims
+  kcache fp4   [num_pages, 64, 416]      uint8 token records:
+                 256 bytes of E2M1 pairs | 32 UE4M3 scales (one per 16
+                 values) | 64 bf16 RoPE dims
   block_table  [B, max_pages]            int32, unused slots -1
   cache_seqlens[B]                       int32
   indices      [B, s_q, topk]            int32 token positions, -1 = ignored
@@ -39,6 +42,7 @@ D_V = 512
 D_ROPE = D_QK - D_V
 FP8_TILE = 128
 FP8_RECORD_BYTES = D_V + 4 * (D_V // FP8_TILE) + 2 * D_ROPE  # 656
+FP4_RECORD_BYTES = D_V // 2 + D_V // 16 + 2 * D_ROPE          # 416
 E4M3_MAX = 448.0
 NVFP4_D = 512                 # NVFP4 rows: 512 values, the whole row is K and V
 NVFP4_BLOCK = 16              # values per UE4M3 scale
@@ -53,7 +57,7 @@ class Workload:
     h_q: int
     seqlens: list
     causal: bool
-    kv: str = "bf16"            # "bf16" | "fp8" | "nvfp4"
+    kv: str = "bf16"            # "bf16" | "fp8" | "nvfp4" | "fp4"
     topk: int = 0               # >0: token-sparse decode
     neg_frac: float = 0.0       # fraction of index slots set to -1
     scale: float = 1.0 / math.sqrt(D_QK)
@@ -141,7 +145,7 @@ def _normal_f32(rng: np.random.Generator, shape) -> torch.Tensor:
 class DecodeInputs:
     workload: Workload
     q: torch.Tensor                   # [B, s_q, h_q, 576] bf16
-    kcache: torch.Tensor              # bf16 [P,64,1,576] or uint8 [P,64,656]
+    kcache: torch.Tensor              # bf16 [P,64,1,576] or uint8 [P,64,656 or 416]
     block_table: torch.Tensor         # [B, max_pages] int32
     cache_seqlens: torch.Tensor       # [B] int32
     indices: Optional[torch.Tensor] = None   # [B, s_q, topk] int32
@@ -199,6 +203,14 @@ def quantize_nvfp4(src: torch.Tensor):
     return packed, sc8.view(torch.uint8).contiguous()
 
 
+def quantize_fp4_records(src: torch.Tensor) -> torch.Tensor:
+    """fp32 [P, 64, 576] source -> uint8 [P, 64, 416] token records: the 512
+    latent dims as in quantize_nvfp4, the 64 RoPE dims as bf16."""
+    codes, sc = quantize_nvfp4(src[..., :D_V])
+    rope = src[..., D_V:].to(torch.bfloat16).contiguous().view(torch.uint8)
+    return torch.cat([codes, sc, rope], dim=-1).contiguous()
+
+
 def make_inputs(w: Workload, *, poison_tail: bool = False, extra_pages: int = 0,
                 seqlens_override=None) -> DecodeInputs:
     """Build the seeded host-side inputs of one workload.
@@ -243,6 +255,14 @@ def make_inputs(w: Workload, *, poison_tail: bool = False, extra_pages: int = 0,
                     kc[int(bt[b, npages[b] - 1]), seqlens[b] % PAGE:] = nan
             for p in perm[P_used:]:
                 kc[int(p)] = nan
+    elif w.kv == "fp4":
+        kc = quantize_fp4_records(_normal_f32(rng, (P, PAGE, D_QK)))
+        if poison_tail:   # NaN scales, RoPE dims of 3.4e38
+            for b in range(B):
+                if npages[b] and seqlens[b] % PAGE:
+                    kc[int(bt[b, npages[b] - 1]), seqlens[b] % PAGE:, D_V // 2:] = 0x7F
+            for p in perm[P_used:]:
+                kc[int(p), :, D_V // 2:] = 0x7F
     else:
         src = _normal_f32(rng, (P, PAGE, D_QK))
         kc = quantize_fp8_records(src)
@@ -290,11 +310,12 @@ def algorithmic_work(inp: DecodeInputs) -> dict:
     FLOPs = 2 * sum over (request, query row, head) of |key set| * (d_qk + 512)
     (d_qk 576, or 512 for NVFP4 rows), counting only unmasked, non-ignored
     keys. Bytes = distinct cache rows touched (1152 B bf16 / 656 B fp8 / 288 B
-    nvfp4) + q + out + lse + block table, seqlens and indices read.
+    nvfp4 / 416 B fp4) + q + out + lse + block table, seqlens and indices read.
     """
     w = inp.workload
     seqlens = inp.cache_seqlens.tolist()
-    row_bytes = {"bf16": 2 * D_QK, "fp8": FP8_RECORD_BYTES, "nvfp4": NVFP4_D // 2 + NVFP4_D // NVFP4_BLOCK}[w.kv]
+    row_bytes = {"bf16": 2 * D_QK, "fp8": FP8_RECORD_BYTES, "nvfp4": NVFP4_D // 2 + NVFP4_D // NVFP4_BLOCK,
+                 "fp4": FP4_RECORD_BYTES}[w.kv]
     d_qk = w.d_qk
     q_bytes = 2 * D_QK if w.kv != "nvfp4" else NVFP4_D // 2 + NVFP4_D // NVFP4_BLOCK
     keys = 0
