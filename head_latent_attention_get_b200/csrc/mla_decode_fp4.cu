@@ -25,7 +25,7 @@
 namespace mla {
 namespace {
 
-constexpr int kN = 8;                  // ring slots of 16 KB
+constexpr int kN = 6;                  // ring slots of 16 KB
 constexpr int kQBytes = 9 * 8192;      // 64 rows x 576 dims
 constexpr int kTmemCols = 512;
 constexpr int kTmemS = 256;            // S buffers at columns 256 and 384
@@ -49,7 +49,8 @@ template <int NR>
 struct Smem {
   static constexpr int q = 0;
   static constexpr int ring = q + kQBytes;
-  static constexpr int pt = ring + kN * fp4::kSlot;
+  static constexpr int stage = ring + kN * fp4::kSlot;
+  static constexpr int pt = stage + fp4::kStageBytes;
   static constexpr int pt_bytes = NR * 256;  // [NR rows][128 tokens] f16
   static constexpr int ctrl = pt + pt_bytes;
   static constexpr int rows = ctrl + 1024;
@@ -82,6 +83,7 @@ __global__ void __launch_bounds__(fp4::kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem + L::q;
   uint8_t* sRing = smem + L::ring;
+  uint4* sStage = reinterpret_cast<uint4*>(smem + L::stage);
   uint8_t* sP = smem + L::pt;
   Ctrl* c = reinterpret_cast<Ctrl*>(smem + L::ctrl);
   fp4::RowTable* rt = reinterpret_cast<fp4::RowTable*>(smem + L::rows);
@@ -142,8 +144,8 @@ __global__ void __launch_bounds__(fp4::kThreads, 1)
   } else if (warp == 3) {
     fp4::row_warp<false, SPARSE>(p, it, rt, lane, wait);
   } else if (warp >= 8) {
-    fp4::convert_ring<false>(p, it, rt, sRing, c->empty, kN, warp - 8, lane, 0, wait,
-                             [&](int slot) { mbar_arrive(&c->full[slot]); });
+    fp4::convert_ring<false>(p, it, rt, sRing, sStage, c->empty, kN, warp - 8, lane, 0, wait,
+                             [&](int slot) { return &c->full[slot]; });
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer: S(0), S(1), O(0), S(2), O(1), ...
     if (lane == 0) {

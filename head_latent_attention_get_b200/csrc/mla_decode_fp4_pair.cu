@@ -28,7 +28,7 @@
 namespace mla {
 namespace fp4pair {
 
-constexpr int kN = 7;                // ring slots of 16 KB
+constexpr int kN = 5;                // ring slots of 16 KB
 constexpr int kQBytes = 9 * 8192;    // 64 rows x 576 dims
 constexpr int kPBytes = 4 * 8192;    // 64 rows x 256 tokens (one buffer)
 constexpr int kTmemCols = 512;
@@ -56,7 +56,8 @@ static_assert(sizeof(Ctrl) <= 2048, "control block");
 struct Smem {
   static constexpr int q = 0;
   static constexpr int ring = q + kQBytes;
-  static constexpr int pt = ring + kN * fp4::kSlot;
+  static constexpr int stage = ring + kN * fp4::kSlot;
+  static constexpr int pt = stage + fp4::kStageBytes;
   static constexpr int ctrl = pt + kPBytes;
   static constexpr int rows = ctrl + 2048;
   static constexpr int total = rows + (int)sizeof(fp4::RowTable);
@@ -107,6 +108,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem + Smem::q;
   uint8_t* sRing = smem + Smem::ring;
+  uint4* sStage = reinterpret_cast<uint4*>(smem + Smem::stage);
   uint8_t* sP = smem + Smem::pt;
   Ctrl* c = reinterpret_cast<Ctrl*>(smem + Smem::ctrl);
   fp4::RowTable* rt = reinterpret_cast<fp4::RowTable*>(smem + Smem::rows);
@@ -175,8 +177,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
   } else if (warp == 2) {
     fp4::row_warp<true, SPARSE>(p, it, rt, lane, wait);
   } else if (warp >= 8) {
-    fp4::convert_ring<true>(p, it, rt, sRing, c->empty, kN, warp - 8, lane, (int)pr.rank, wait,
-                            [&](int slot) { mbar_arrive(pr.leader ? &c->full[slot] : &c->v_loc[slot]); });
+    fp4::convert_ring<true>(p, it, rt, sRing, sStage, c->empty, kN, warp - 8, lane, (int)pr.rank, wait,
+                            [&](int slot) { return pr.leader ? &c->full[slot] : &c->v_loc[slot]; });
   } else if (warp == 1 && !pr.leader) {
     // ------------------------------------------------------------ odd CTA: forward slot completions
     if (lane == 0) {

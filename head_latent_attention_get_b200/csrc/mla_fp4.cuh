@@ -9,12 +9,12 @@
 // f16 too). Both are exact: an E2M1 x UE4M3 product has at most 6 significant
 // bits and lies in [2^-10, 2688].
 //
-// Nothing raw is staged in shared memory. A converter thread keeps the codes
-// of the next eight slots in registers: slot i of a phase is converted, and
-// its register then takes slot i of the phase after it, so a load has a whole
-// phase (eight slots) to arrive. Reading the codes again for V costs 256 bytes
-// a token from L2, a quarter of what the bf16 cache's V re-read costs, and
-// leaves all shared memory beside Q and P to the ring.
+// A converter thread stages the 16 code bytes of its next eight slots in shared
+// memory of its own (cp.async, no other thread touches them): slot i of a
+// phase is converted, then its 16 bytes are refilled for slot i of the phase
+// after it, so a copy has a whole phase to arrive. Scales take registers, also
+// one phase ahead. Reading the codes again for V costs 256 bytes a token from
+// L2, a quarter of the bf16 cache's V re-read.
 #pragma once
 #include <cuda_fp16.h>
 
@@ -27,6 +27,7 @@ constexpr int kSlot = 16384;     // a K slice (128 tokens x 64 dims) or a V slot
 constexpr int kCvWarps = 8;
 constexpr int kRowDepth = 4;     // steps whose cache rows are resolved ahead
 constexpr int kThreads = 256 + 32 * kCvWarps;
+constexpr int kStageBytes = 8 * 32 * kCvWarps * 16;
 
 // Ring order of a piece of n steps: h = 0 -> K of step 0; h = 2g+1 -> K of
 // step g+1 (only if g+1 < n); h = 2g+2 -> V of step g. A K entry is nine
@@ -127,27 +128,11 @@ __device__ __forceinline__ __half2 ue4m3x2(uint32_t s) {
   return *reinterpret_cast<const __half2*>(&hr);
 }
 
-// 32 codes and their two scales.
-struct Item {
-  uint4 c;
-  uint32_t s;
-};
-__device__ __forceinline__ Item load_item(const uint8_t* cache, int row, int dim0) {
-  Item it;
-  it.c = make_uint4(0, 0, 0, 0);
-  it.s = 0;
-  if (row >= 0) {
-    const uint8_t* rec = cache + (size_t)row * kFp4RecordBytes;
-    it.c = ldg16(rec + dim0 / 2);
-    it.s = *reinterpret_cast<const uint16_t*>(rec + kFp4ScaleOff + dim0 / 16);
-  }
-  return it;
-}
-// Writes the item's 32 values as chunks c0..c0+3 of 128-byte row `row` of a swizzled tile.
+// 32 codes and their two scale bytes as chunks c0..c0+3 of 128-byte row `row` of a swizzled tile.
 template <bool K>
-__device__ __forceinline__ void store_item(const Item& it, uint8_t* tile, int row, int c0) {
-  const __half2 sc = ue4m3x2(it.s);
-  const uint32_t w[4] = {it.c.x, it.c.y, it.c.z, it.c.w};
+__device__ __forceinline__ void store_item(uint4 codes, uint32_t scales, uint8_t* tile, int row, int c0) {
+  const __half2 sc = ue4m3x2(scales);
+  const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const __half s1 = i < 2 ? __low2half(sc) : __high2half(sc);
@@ -156,6 +141,12 @@ __device__ __forceinline__ void store_item(const Item& it, uint8_t* tile, int ro
     else v = e2m1x8_to_f16(w[i], __half2half2(s1));
     *reinterpret_cast<uint4*>(sw128(tile, row, c0 + i)) = v;
   }
+}
+// Copies a loaded word with an instruction that the compiler keeps where it is.
+__device__ __forceinline__ uint32_t settle(uint32_t a) {
+  uint32_t b;
+  asm volatile("mov.b32 %0, %1;" : "=r"(b) : "r"(a));
+  return b;
 }
 
 // ---------------------------------------------------------------- row warp
@@ -204,34 +195,60 @@ __device__ __forceinline__ void row_warp(const DecodeParams& p, PieceIter it, Ro
 // (token 16 cw + lane % 16, half lane / 16 of the slice's 64 dims); V slot:
 // thread (token 8 cw + lane % 8, quarter lane / 8 of the slot's 128 dims);
 // eight neighbouring lanes write the same chunk of eight rows, which the
-// swizzle spreads over all banks. The RoPE slice goes straight into its slot
-// with cp.async and is handed over after the next phase's second slot.
-// wait(bar, parity): the kernel's bounded wait; full(slot): one lane per warp
-// hands the slot over.
+// swizzle spreads over all banks. `stage`: [8 items][256 threads] of 16 bytes.
+// The RoPE slice goes straight into its slot with cp.async, whose completion
+// the slot's barrier counts.
+// wait(bar, parity): the kernel's bounded wait; full(slot): the slot's barrier.
 template <bool PAIR, class Wait, class Full>
 __device__ __forceinline__ void convert_ring(const DecodeParams& p, const PieceIter& it, RowTable* rt, uint8_t* ring,
-                                             uint64_t* empty, int nslots, int cw, int lane, int rank, Wait wait,
-                                             Full full) {
+                                             uint4* stage, uint64_t* empty, int nslots, int cw, int lane, int rank,
+                                             Wait wait, Full full) {
   const uint8_t* cache = static_cast<const uint8_t*>(p.kcache);
   const int ktok = 16 * cw + (lane & 15), khalf = lane >> 4;
   const int vtok = 8 * cw + (lane & 7), vq = lane >> 3;
-  auto load = [&](const Phases<PAIR>& ph, int i) {
-    const int32_t* rows = rt->row[ph.step() % kRowDepth];
-    if (ph.is_k()) return load_item(cache, rows[(PAIR ? 128 * rank : 0) + ktok], 64 * i + 32 * khalf);
-    // V slot i: a pair's (64-token quarter i / 2, value dims 256 (i % 2) + 128 rank ..),
-    // a single CTA's (value dims 128 (i / 2) .., 64-token half i % 2)
-    const int tq = PAIR ? i >> 1 : i & 1, d0 = PAIR ? 256 * (i & 1) + 128 * rank : 128 * (i >> 1);
-    return load_item(cache, rows[64 * tq + vtok], d0 + 32 * vq);
+  stage += 32 * cw + lane;
+  // V slot i: a pair's (64-token quarter i / 2, value dims 256 (i % 2) + 128 rank ..),
+  // a single CTA's (value dims 128 (i / 2) .., 64-token half i % 2)
+  auto vrow = [&](int i) { return 64 * (PAIR ? i >> 1 : i & 1) + vtok; };
+  auto vdim = [&](int i) { return (PAIR ? 256 * (i & 1) + 128 * rank : 128 * (i >> 1)) + 32 * vq; };
+  auto rows_of = [&](int step) { return static_cast<const int32_t*>(rt->row[step % kRowDepth]); };
+  const int k0 = PAIR ? 128 * rank : 0;  // first token of this CTA's K tile
+  // codes of item i of a phase -> the thread's own 16 bytes of stage i
+  auto fetch = [&](bool k, int step, int i) {
+    const int row = rows_of(step)[k ? k0 + ktok : vrow(i)];
+    const uint8_t* src = cache + (size_t)(row >= 0 ? row : 0) * kFp4RecordBytes + (k ? 64 * i + 32 * khalf : vdim(i)) / 2;
+    cp_async16(stage + i * 256, src, row >= 0 ? 16u : 0u);
+  };
+  // the two scale bytes of each item of a phase, in the low half of sc[i]
+  auto scales = [&](bool k, int step, uint32_t (&sc)[8]) {
+    if (k) {
+      const int row = rows_of(step)[k0 + ktok];
+      uint4 a = make_uint4(0, 0, 0, 0), b = a;
+      if (row >= 0) {
+        const uint8_t* src = cache + (size_t)row * kFp4RecordBytes + kFp4ScaleOff;
+        a = ldg16(src);
+        b = ldg16(src + 16);
+      }
+      sc[0] = a.x, sc[1] = a.y, sc[2] = a.z, sc[3] = a.w, sc[4] = b.x, sc[5] = b.y, sc[6] = b.z, sc[7] = b.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int row = rows_of(step)[vrow(i)];
+        sc[i] = 0;
+        if (row >= 0)
+          sc[i] = *reinterpret_cast<const uint16_t*>(cache + (size_t)row * kFp4RecordBytes + kFp4ScaleOff + vdim(i) / 16);
+      }
+    }
   };
   auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
     bool ok = true;
     if (lane == 0) ok = wait(bar, parity);
     return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
   };
-  Phases<PAIR> nxt;  // the phase being loaded, one ahead of the phase being converted
+  Phases<PAIR> nxt;  // the phase being fetched, one ahead of the phase being converted
   nxt.it = it;
-  Item buf[8];
-  int slot = 0, rope_slot = -1;
+  uint32_t pre[8];   // its scales
+  int slot = 0;
   uint32_t par = 1;  // parity to wait for on the slot's empty barrier
   auto advance = [&] {
     if (++slot == nslots) {
@@ -239,60 +256,64 @@ __device__ __forceinline__ void convert_ring(const DecodeParams& p, const PieceI
       par ^= 1;
     }
   };
-  auto retire_rope = [&] {
-    cp_async_wait<0>();
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) full(rope_slot);
-    rope_slot = -1;
-  };
   bool have = nxt.next();
   if (have) {
     if (!wait_warp(&rt->full[0], 0)) return;
+    scales(true, 0, pre);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) buf[i] = load(nxt, i);
+    for (int i = 0; i < 8; ++i) {
+      fetch(true, 0, i);
+      cp_async_commit();
+    }
   }
   bool stop = false;
   while (have && !stop) {
     const bool k = nxt.is_k();
     const int step = nxt.step();
     have = nxt.next();
-    if (have && nxt.is_k()) {
-      const int s = nxt.step();
-      if (!wait_warp(&rt->full[s % kRowDepth], (s / kRowDepth) & 1)) break;
-    }
+    const bool nk = have && nxt.is_k();
+    const int nstep = nxt.step();
+    if (nk && !wait_warp(&rt->full[nstep % kRowDepth], (nstep / kRowDepth) & 1)) break;
+    // one wait for all scales: loads share a few scoreboards, so one used
+    // while younger loads are in flight would wait for those too
+    uint32_t sc[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sc[i] = settle(pre[i]);
+    if (have) scales(nk, nstep, pre);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       if (!wait_warp(&empty[slot], par)) { stop = true; break; }
+      cp_async_wait<7>();  // one group per item: the seven younger ones may be in flight
+      const uint4 codes = stage[i * 256];
       uint8_t* s = ring + slot * kSlot;
-      if (k) store_item<true>(buf[i], s, ktok, 4 * khalf);
-      else store_item<false>(buf[i], s + (vq >> 1) * 8192, vtok, 4 * (vq & 1));
+      if (k) store_item<true>(codes, khalf ? sc[i] >> 16 : sc[i], s, ktok, 4 * khalf);
+      else store_item<false>(codes, sc[i], s + (vq >> 1) * 8192, vtok, 4 * (vq & 1));
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) full(slot);
+      if (lane == 0) mbar_arrive(full(slot));
       advance();
-      if (have) buf[i] = load(nxt, i);
-      if (i == 1 && rope_slot >= 0) retire_rope();
+      if (have) fetch(nk, nstep, i);
+      cp_async_commit();
     }
     if (stop) break;
     if (k) {  // RoPE slice: 8 lanes per 128-byte row
       if (!wait_warp(&empty[slot], par)) break;
-      const int32_t* rows = rt->row[step % kRowDepth] + (PAIR ? 128 * rank : 0);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int t = 16 * cw + 4 * i + (lane >> 3), ch = lane & 7;
-        const int row = rows[t];
+        const int row = rows_of(step)[k0 + t];
         cp_async16(sw128(ring + slot * kSlot, t, ch),
                    cache + (size_t)(row >= 0 ? row : 0) * kFp4RecordBytes + kFp4RopeOff + 16 * ch, row >= 0 ? 16u : 0u);
       }
-      cp_async_commit();
-      rope_slot = slot;
+      cp_async_mbar_arrive(full(slot));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full(slot));
       advance();
     }
-    // the rows of a step are last read by the loads of its V entry
-    if (have && !nxt.is_k()) {
+    // the rows of a step are last read by the fetches of its V entry
+    if (have && !nk) {
       __syncwarp();
-      if (lane == 0) mbar_arrive(&rt->empty[nxt.step() % kRowDepth]);
+      if (lane == 0) mbar_arrive(&rt->empty[nstep % kRowDepth]);
     }
   }
   cp_async_wait<0>();  // no copy may land after the CTA has finished
