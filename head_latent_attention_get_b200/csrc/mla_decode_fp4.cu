@@ -59,6 +59,7 @@ struct Smem {
 static_assert(Smem<64>::total + 1024 <= 232448, "shared memory budget");
 
 __device__ __forceinline__ bool timed_wait(Ctrl* c, uint64_t* bar, uint32_t parity, const DecodeParams& p) {
+  if (mbar_try_wait(bar, parity)) return true;
   if (*(volatile int*)&c->abort_flag) return false;
   if (mbar_wait(bar, parity, p.timeout_ns)) return true;
   atomicOr(p.status, (uint32_t)MLA_DEVICE_STATUS_TIMEOUT);
@@ -95,7 +96,7 @@ __global__ void __launch_bounds__(fp4::kThreads, 1)
   if (threadIdx.x == 0) {
     mbar_init(&c->q_full, 1);
     mbar_init(&c->q_empty, 1);
-    for (int i = 0; i < kN; ++i) { mbar_init(&c->full[i], fp4::kCvWarps); mbar_init(&c->empty[i], 1); }
+    for (int i = 0; i < kN; ++i) { mbar_init(&c->full[i], 4); mbar_init(&c->empty[i], 1); }
     for (int i = 0; i < 2; ++i) mbar_init(&c->s_full[i], 1);
     for (int i = 0; i < fp4::kRowDepth; ++i) {
       mbar_init(&rt->full[i], 1);
@@ -144,13 +145,17 @@ __global__ void __launch_bounds__(fp4::kThreads, 1)
   } else if (warp == 3) {
     fp4::row_warp<false, SPARSE>(p, it, rt, lane, wait);
   } else if (warp >= 8) {
-    fp4::convert_ring<false>(p, it, rt, sRing, sStage, c->empty, kN, warp - 8, lane, 0, wait,
+    fp4::convert_ring<false, kN>(p, it, rt, sRing, sStage, c->empty, warp - 8, lane, 0, wait,
                              [&](int slot) { return &c->full[slot]; });
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer: S(0), S(1), O(0), S(2), O(1), ...
     if (lane == 0) {
       const uint32_t idesc_s = idesc_bf16(64, 128, false, false);
       const uint32_t idesc_o = idesc_f16(128, NR, true, false);
+      // descriptors: Q, K slots and P^T are K-major, V slots MN-major (halves 8 KB apart)
+      const uint32_t q_lo = sdesc_lo(smem_u32(sQ), 16), k_lo = sdesc_lo(smem_u32(sRing), 16);
+      const uint32_t v_lo = sdesc_lo(smem_u32(sRing), 8192), p_lo = sdesc_lo(smem_u32(sP), 16);
+      constexpr uint32_t d_hi = sdesc_hi(1024);
       int sc = 0, gs = 0, go = 0, pi = 0;
       bool stop = false;
       while (!stop && it.next(pc)) {
@@ -167,11 +172,11 @@ __global__ void __launch_bounds__(fp4::kThreads, 1)
               const int slot = sc % kN;
               if (!timed_wait(c, &c->full[slot], (sc / kN) & 1, p)) { stop = true; break; }
               tc_fence_after();
-              const uint32_t qa = smem_u32(sQ + j * 8192), kb = smem_u32(sRing + slot * fp4::kSlot);
+              const uint32_t qa = q_lo + j * (8192 >> 4), kb = k_lo + slot * (fp4::kSlot >> 4);
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
-                mma_bf16_ss(d, sdesc(qa + kk * 32, 16, 1024), sdesc(kb + kk * 32, 16, 1024), idesc_s,
-                           (j | kk) != 0 ? 1u : 0u);
+                mma_bf16_ss(d, sdesc_join(qa + kk * 2, d_hi), sdesc_join(kb + kk * 2, d_hi), idesc_s,
+                            (j | kk) != 0 ? 1u : 0u);
               mma_commit(&c->empty[slot]);
             }
             if (stop) break;
@@ -182,16 +187,15 @@ __global__ void __launch_bounds__(fp4::kThreads, 1)
             const bool first = g == 0;
             if (first && pi > 0 && !timed_wait(c, &c->o_free, (pi - 1) & 1, p)) { stop = true; break; }
             if (!timed_wait(c, &c->p_full, go & 1, p)) { stop = true; break; }
-            const uint32_t pt = smem_u32(sP);
             for (int j = 0; j < 8; ++j, ++sc) {  // value dims 128 (j / 2) .., token half j % 2
               const int slot = sc % kN, m = j >> 1, hf = j & 1;
               if (!timed_wait(c, &c->full[slot], (sc / kN) & 1, p)) { stop = true; break; }
               tc_fence_after();
-              const uint32_t va = smem_u32(sRing + slot * fp4::kSlot);
+              const uint32_t va = v_lo + slot * (fp4::kSlot >> 4), pa = p_lo + hf * (NR * 128 >> 4);
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
-                mma_bf16_ss(tmem + 64 * m, sdesc(va + kk * 2048, 8192, 1024), sdesc(pt + hf * (NR * 128) + kk * 32, 16, 1024),
-                           idesc_o, (first && hf == 0 && kk == 0) ? 0u : 1u);
+                mma_bf16_ss(tmem + 64 * m, sdesc_join(va + kk * (2048 >> 4), d_hi), sdesc_join(pa + kk * 2, d_hi), idesc_o,
+                            (first && hf == 0 && kk == 0) ? 0u : 1u);
               mma_commit(&c->empty[slot]);
             }
             if (stop) break;

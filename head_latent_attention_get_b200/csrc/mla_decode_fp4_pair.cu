@@ -82,6 +82,7 @@ __device__ __forceinline__ bool aborted(const Pair& pr) { return *(volatile int*
 // Bounded wait with cluster-scope acquire (several barriers receive arrivals
 // from the other CTA or pair-MMA commits).
 __device__ __forceinline__ bool pwait(const Pair& pr, uint64_t* bar, uint32_t parity, const DecodeParams& p) {
+  if (mbar_try_wait_cluster(bar, parity)) return true;
   if (aborted(pr)) return false;
   if (mbar_wait_cluster(bar, parity, p.timeout_ns)) return true;
   raise_abort(pr, p);
@@ -124,7 +125,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
 
   if (threadIdx.x == 0) {
     mbar_init(&c->q_full, 1);
-    for (int i = 0; i < kN; ++i) mbar_init(&c->full[i], fp4::kCvWarps + 1);
+    for (int i = 0; i < kN; ++i) mbar_init(&c->full[i], 4 + 1);
     for (int i = 0; i < 2; ++i) mbar_init(&c->p_full[i], 8);
     mbar_init(&c->o_free, 8);
     mbar_init(&c->drain, 1);
@@ -132,7 +133,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
     for (int i = 0; i < kN; ++i) mbar_init(&c->empty[i], 1);
     for (int i = 0; i < 2; ++i) mbar_init(&c->s_full[i], 1);
     for (int i = 0; i < 2; ++i) mbar_init(&c->o_done[i], 1);
-    for (int i = 0; i < kN; ++i) mbar_init(&c->v_loc[i], fp4::kCvWarps);
+    for (int i = 0; i < kN; ++i) mbar_init(&c->v_loc[i], 4);
     for (int i = 0; i < fp4::kRowDepth; ++i) {
       mbar_init(&rt->full[i], 1);
       mbar_init(&rt->empty[i], fp4::kCvWarps + (SPARSE ? 4 : 0));
@@ -177,7 +178,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
   } else if (warp == 2) {
     fp4::row_warp<true, SPARSE>(p, it, rt, lane, wait);
   } else if (warp >= 8) {
-    fp4::convert_ring<true>(p, it, rt, sRing, sStage, c->empty, kN, warp - 8, lane, (int)pr.rank, wait,
+    fp4::convert_ring<true, kN>(p, it, rt, sRing, sStage, c->empty, warp - 8, lane, (int)pr.rank, wait,
                             [&](int slot) { return pr.leader ? &c->full[slot] : &c->v_loc[slot]; });
   } else if (warp == 1 && !pr.leader) {
     // ------------------------------------------------------------ odd CTA: forward slot completions
@@ -200,6 +201,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
     // ------------------------------------------------------------ MMA issuer: S(0), S(1), O(0), S(2), O(1), ...
     const uint32_t idesc_s = idesc_bf16(128, 256, false, false);
     const uint32_t idesc_o = idesc_f16(128, 256, false, true);
+    // descriptors: Q, K slots and P are K-major, V slots MN-major (halves 8 KB apart)
+    const uint32_t q_lo = sdesc_lo(smem_u32(sQ), 16), k_lo = sdesc_lo(smem_u32(sRing), 16);
+    const uint32_t v_lo = sdesc_lo(smem_u32(sRing), 8192), p_lo = sdesc_lo(smem_u32(sP), 16);
+    constexpr uint32_t d_hi = sdesc_hi(1024);
     int sc = 0, gs = 0, go = 0, pi = 0;
     bool stop = false;
     if (lane == 0) {
@@ -219,10 +224,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
               const int slot = sc % kN;
               if (!pwait(pr, &c->full[slot], (sc / kN) & 1, p)) { stop = true; break; }
               tc_fence_after();
-              const uint32_t qa = smem_u32(sQ + j * 8192), kb = smem_u32(sRing + slot * fp4::kSlot);
+              const uint32_t qa = q_lo + j * (8192 >> 4), kb = k_lo + slot * (fp4::kSlot >> 4);
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
-                mma_bf16_ss_pair(d, sdesc(qa + kk * 32, 16, 1024), sdesc(kb + kk * 32, 16, 1024), idesc_s,
+                mma_bf16_ss_pair(d, sdesc_join(qa + kk * 2, d_hi), sdesc_join(kb + kk * 2, d_hi), idesc_s,
                                  (j | kk) != 0 ? 1u : 0u);
               mma_commit_pair(&c->empty[slot]);
             }
@@ -234,17 +239,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
             const bool first = g == 0;
             if (first && pi > 0 && !pwait(pr, &c->o_free, (pi - 1) & 1, p)) { stop = true; break; }
             if (!pwait(pr, &c->p_full[go & 1], (go >> 1) & 1, p)) { stop = true; break; }
-            const uint32_t pt = smem_u32(sP);
             for (int q = 0; q < 4 && !stop; ++q) {
               for (int jd = 0; jd < 2; ++jd, ++sc) {
                 const int slot = sc % kN;
                 if (!pwait(pr, &c->full[slot], (sc / kN) & 1, p)) { stop = true; break; }
                 tc_fence_after();
-                const uint32_t va = smem_u32(sRing + slot * fp4::kSlot);
+                const uint32_t va = v_lo + slot * (fp4::kSlot >> 4), pa = p_lo + q * (8192 >> 4);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                  mma_bf16_ss_pair(tmem + 128 * jd, sdesc(pt + q * 8192 + kk * 32, 16, 1024),
-                                   sdesc(va + kk * 2048, 8192, 1024), idesc_o, (first && q == 0 && kk == 0) ? 0u : 1u);
+                  mma_bf16_ss_pair(tmem + 128 * jd, sdesc_join(pa + kk * 2, d_hi), sdesc_join(va + kk * (2048 >> 4), d_hi),
+                                   idesc_o, (first && q == 0 && kk == 0) ? 0u : 1u);
                 mma_commit_pair(&c->empty[slot]);
               }
             }

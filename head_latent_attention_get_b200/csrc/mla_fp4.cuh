@@ -24,10 +24,11 @@ namespace mla {
 namespace fp4 {
 
 constexpr int kSlot = 16384;     // a K slice (128 tokens x 64 dims) or a V slot (64 tokens x 128 dims, two halves)
-constexpr int kCvWarps = 8;
+constexpr int kGroups = 2;       // converter groups of four warps
+constexpr int kCvWarps = 4 * kGroups;
 constexpr int kRowDepth = 4;     // steps whose cache rows are resolved ahead
 constexpr int kThreads = 256 + 32 * kCvWarps;
-constexpr int kStageBytes = 8 * 32 * kCvWarps * 16;
+constexpr int kStageBytes = 8 * 4096;  // the code bytes of eight slots
 
 // Ring order of a piece of n steps: h = 0 -> K of step 0; h = 2g+1 -> K of
 // step g+1 (only if g+1 < n); h = 2g+2 -> V of step g. A K entry is nine
@@ -191,78 +192,77 @@ __device__ __forceinline__ void row_warp(const DecodeParams& p, PieceIter it, Ro
 }
 
 // ---------------------------------------------------------------- converters
-// Fills the ring, one item of 32 codes per thread and slot. K slot: thread
-// (token 16 cw + lane % 16, half lane / 16 of the slice's 64 dims); V slot:
-// thread (token 8 cw + lane % 8, quarter lane / 8 of the slot's 128 dims);
-// eight neighbouring lanes write the same chunk of eight rows, which the
-// swizzle spreads over all banks. `stage`: [8 items][256 threads] of 16 bytes.
+// Fills the ring. Groups of four warps take the slots of a phase in turn
+// (group g: latent slots g, g + kGroups, ..; group 0 also copies the RoPE
+// slice), so that the waits of one group hide behind the arithmetic of the
+// others. A thread converts two items of 32 codes per slot. K slot: tokens
+// 32 w + 16 j + lane % 16, half lane / 16 of the slice's 64 dims; V slot:
+// tokens 16 w + 8 j + lane % 8, quarter lane / 8 of the slot's 128 dims; eight
+// neighbouring lanes write the same chunk of eight rows, which the swizzle
+// spreads over all banks. `stage`: 16 bytes per item and thread.
 // The RoPE slice goes straight into its slot with cp.async, whose completion
 // the slot's barrier counts.
 // wait(bar, parity): the kernel's bounded wait; full(slot): the slot's barrier.
-template <bool PAIR, class Wait, class Full>
+template <bool PAIR, int NSLOTS, class Wait, class Full>
 __device__ __forceinline__ void convert_ring(const DecodeParams& p, const PieceIter& it, RowTable* rt, uint8_t* ring,
-                                             uint4* stage, uint64_t* empty, int nslots, int cw, int lane, int rank,
-                                             Wait wait, Full full) {
+                                             uint4* stage, uint64_t* empty, int cw, int lane, int rank, Wait wait,
+                                             Full full) {
+  constexpr int kPer = 8 / kGroups;  // latent slots of a phase per group
   const uint8_t* cache = static_cast<const uint8_t*>(p.kcache);
-  const int ktok = 16 * cw + (lane & 15), khalf = lane >> 4;
-  const int vtok = 8 * cw + (lane & 7), vq = lane >> 3;
-  stage += 32 * cw + lane;
-  // V slot i: a pair's (64-token quarter i / 2, value dims 256 (i % 2) + 128 rank ..),
-  // a single CTA's (value dims 128 (i / 2) .., 64-token half i % 2)
-  auto vrow = [&](int i) { return 64 * (PAIR ? i >> 1 : i & 1) + vtok; };
-  auto vdim = [&](int i) { return (PAIR ? 256 * (i & 1) + 128 * rank : 128 * (i >> 1)) + 32 * vq; };
-  auto rows_of = [&](int step) { return static_cast<const int32_t*>(rt->row[step % kRowDepth]); };
+  const int grp = cw >> 2, w = cw & 3;
+  const int ktok = 32 * w + (lane & 15), khalf = lane >> 4;
+  const int vtok = 16 * w + (lane & 7), vq = lane >> 3;
   const int k0 = PAIR ? 128 * rank : 0;  // first token of this CTA's K tile
-  // codes of item i of a phase -> the thread's own 16 bytes of stage i
-  auto fetch = [&](bool k, int step, int i) {
-    const int row = rows_of(step)[k ? k0 + ktok : vrow(i)];
-    const uint8_t* src = cache + (size_t)(row >= 0 ? row : 0) * kFp4RecordBytes + (k ? 64 * i + 32 * khalf : vdim(i)) / 2;
-    cp_async16(stage + i * 256, src, row >= 0 ? 16u : 0u);
+  stage += 32 * cw + lane;
+  // record and first dim of item (i, j) of a phase; V slot i is a pair's
+  // (64-token quarter i / 2, value dims 256 (i % 2) + 128 rank ..), a single
+  // CTA's (value dims 128 (i / 2) .., 64-token half i % 2)
+  auto row_of = [&](bool k, int step, int i, int j) {
+    const int t = k ? k0 + ktok + 16 * j : 64 * (PAIR ? i >> 1 : i & 1) + vtok + 8 * j;
+    return rt->row[step % kRowDepth][t];
   };
-  // the two scale bytes of each item of a phase, in the low half of sc[i]
-  auto scales = [&](bool k, int step, uint32_t (&sc)[8]) {
-    if (k) {
-      const int row = rows_of(step)[k0 + ktok];
-      uint4 a = make_uint4(0, 0, 0, 0), b = a;
-      if (row >= 0) {
-        const uint8_t* src = cache + (size_t)row * kFp4RecordBytes + kFp4ScaleOff;
-        a = ldg16(src);
-        b = ldg16(src + 16);
-      }
-      sc[0] = a.x, sc[1] = a.y, sc[2] = a.z, sc[3] = a.w, sc[4] = b.x, sc[5] = b.y, sc[6] = b.z, sc[7] = b.w;
-    } else {
+  auto dim_of = [&](bool k, int i) {
+    return k ? 64 * i + 32 * khalf : (PAIR ? 256 * (i & 1) + 128 * rank : 128 * (i >> 1)) + 32 * vq;
+  };
+  auto fetch = [&](bool k, int step, int n) {
+    const int i = grp + kGroups * n, d = dim_of(k, i);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int row = rows_of(step)[vrow(i)];
-        sc[i] = 0;
+    for (int j = 0; j < 2; ++j) {
+      const int row = row_of(k, step, i, j);
+      cp_async16(stage + (2 * n + j) * (32 * kCvWarps), cache + (size_t)(row >= 0 ? row : 0) * kFp4RecordBytes + d / 2,
+                 row >= 0 ? 16u : 0u);
+    }
+  };
+  auto scales = [&](bool k, int step, uint32_t (&sc)[kPer][2]) {
+#pragma unroll
+    for (int n = 0; n < kPer; ++n) {
+      const int i = grp + kGroups * n, d = dim_of(k, i);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int row = row_of(k, step, i, j);
+        sc[n][j] = 0;
         if (row >= 0)
-          sc[i] = *reinterpret_cast<const uint16_t*>(cache + (size_t)row * kFp4RecordBytes + kFp4ScaleOff + vdim(i) / 16);
+          sc[n][j] = *reinterpret_cast<const uint16_t*>(cache + (size_t)row * kFp4RecordBytes + kFp4ScaleOff + d / 16);
       }
     }
   };
   auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
     bool ok = true;
     if (lane == 0) ok = wait(bar, parity);
     return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
   };
-  Phases<PAIR> nxt;  // the phase being fetched, one ahead of the phase being converted
+  Phases<PAIR> nxt;         // the phase being fetched, one ahead of the phase being converted
   nxt.it = it;
-  uint32_t pre[8];   // its scales
-  int slot = 0;
-  uint32_t par = 1;  // parity to wait for on the slot's empty barrier
-  auto advance = [&] {
-    if (++slot == nslots) {
-      slot = 0;
-      par ^= 1;
-    }
-  };
+  uint32_t pre[kPer][2];    // its scales
+  int seq = 0;              // ring position of the converted phase's first slot
   bool have = nxt.next();
   if (have) {
     if (!wait_warp(&rt->full[0], 0)) return;
     scales(true, 0, pre);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      fetch(true, 0, i);
+    for (int n = 0; n < kPer; ++n) {
+      fetch(true, 0, n);
       cp_async_commit();
     }
   }
@@ -276,39 +276,56 @@ __device__ __forceinline__ void convert_ring(const DecodeParams& p, const PieceI
     if (nk && !wait_warp(&rt->full[nstep % kRowDepth], (nstep / kRowDepth) & 1)) break;
     // one wait for all scales: loads share a few scoreboards, so one used
     // while younger loads are in flight would wait for those too
-    uint32_t sc[8];
+    uint32_t sc[kPer][2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sc[i] = settle(pre[i]);
+    for (int n = 0; n < kPer; ++n)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) sc[n][j] = settle(pre[n][j]);
     if (have) scales(nk, nstep, pre);
+    // not unrolled: the unrolled loop's code left no room in the instruction
+    // cache for the other roles
+#pragma unroll 1
+    for (int n = 0; n < kPer; ++n) {
+      const int sq = seq + grp + kGroups * n, slot = sq % NSLOTS;
+      cp_async_wait<kPer - 1>();  // one group per slot: the younger ones may be in flight
+      uint4 codes[2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (!wait_warp(&empty[slot], par)) { stop = true; break; }
-      cp_async_wait<7>();  // one group per item: the seven younger ones may be in flight
-      const uint4 codes = stage[i * 256];
+      for (int j = 0; j < 2; ++j) codes[j] = stage[(2 * n + j) * (32 * kCvWarps)];
+      if (!wait_warp(&empty[slot], ((sq / NSLOTS) & 1) ^ 1)) { stop = true; break; }
       uint8_t* s = ring + slot * kSlot;
-      if (k) store_item<true>(codes, khalf ? sc[i] >> 16 : sc[i], s, ktok, 4 * khalf);
-      else store_item<false>(codes, sc[i], s + (vq >> 1) * 8192, vtok, 4 * (vq & 1));
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        if (k) store_item<true>(codes[j], sc[0][j], s, ktok + 16 * j, 4 * khalf);
+        else store_item<false>(codes[j], sc[0][j], s + (vq >> 1) * 8192, vtok + 8 * j, 4 * (vq & 1));
+      }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(full(slot));
-      advance();
-      if (have) fetch(nk, nstep, i);
+      if (have) fetch(nk, nstep, n);
       cp_async_commit();
+#pragma unroll
+      for (int m = 0; m + 1 < kPer; ++m)  // the next slot's scales move to the front
+#pragma unroll
+        for (int j = 0; j < 2; ++j) sc[m][j] = sc[m + 1][j];
     }
     if (stop) break;
-    if (k) {  // RoPE slice: 8 lanes per 128-byte row
-      if (!wait_warp(&empty[slot], par)) break;
+    seq += 8;
+    if (k) {
+      if (grp == 0) {  // RoPE slice: 8 lanes per 128-byte row
+        const int slot = seq % NSLOTS;
+        if (!wait_warp(&empty[slot], ((seq / NSLOTS) & 1) ^ 1)) break;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int t = 16 * cw + 4 * i + (lane >> 3), ch = lane & 7;
-        const int row = rows_of(step)[k0 + t];
-        cp_async16(sw128(ring + slot * kSlot, t, ch),
-                   cache + (size_t)(row >= 0 ? row : 0) * kFp4RecordBytes + kFp4RopeOff + 16 * ch, row >= 0 ? 16u : 0u);
+        for (int i = 0; i < 8; ++i) {
+          const int t = 32 * w + 4 * i + (lane >> 3), ch = lane & 7;
+          const int row = rt->row[step % kRowDepth][k0 + t];
+          cp_async16(sw128(ring + slot * kSlot, t, ch),
+                     cache + (size_t)(row >= 0 ? row : 0) * kFp4RecordBytes + kFp4RopeOff + 16 * ch, row >= 0 ? 16u : 0u);
+        }
+        cp_async_mbar_arrive(full(slot));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full(slot));
       }
-      cp_async_mbar_arrive(full(slot));
-      __syncwarp();
-      if (lane == 0) mbar_arrive(full(slot));
-      advance();
+      ++seq;
     }
     // the rows of a step are last read by the fetches of its V entry
     if (have && !nk) {
