@@ -3,15 +3,16 @@
 //
 // Same computation and TMEM layout as the row-group kernel of the bf16 cache
 // (mla_decode.cu): per tile of 128 tokens
-//   S    = Q K^T     tcgen05 M=64 rows x N=128 tokens x K=576, bf16
+//   S    = Q K^T     tcgen05 M=64 rows x N=128 tokens x K=576
 //   softmax          one thread per query row, online, O rescaled lazily
-//   O^T += V^T P^T   tcgen05 M=128 value dims (4 chunks) x N=rows x K=128, f16
+//   O^T += V^T P^T   tcgen05 M=128 value dims (4 chunks) x N=rows x K=128
 // The keys reach the tensor core through one ring of 16 KB slots that eight
 // converter warps fill from the records (mla_fp4.cuh), in the order in which
 // the one MMA issuer consumes it: S(0), S(1), O(0), S(2), O(1), ...
 //
 // Warp roles (512 threads):
-//   0 Q via TMA   1 MMA issuer (+ TMEM alloc)   2 idle   3 cache rows
+//   0 Q via TMA, then 0 and 2 put it in the converted keys' order
+//   1 MMA issuer (+ TMEM alloc)   3 cache rows
 //   4-7 softmax + epilogue (row r = 16*(warp-4) + lane, lanes 0-15)
 //   8-15 converters
 // Every wait is bounded; on a timeout the CTA records
@@ -32,7 +33,7 @@ constexpr int kTmemS = 256;            // S buffers at columns 256 and 384
 constexpr float kRescaleLog2 = 8.0f;   // rescale O only when the max grows by > 2^8
 
 struct Ctrl {
-  uint64_t q_full, q_empty;
+  uint64_t q_raw, q_full, q_empty;      // q_raw: as loaded; q_full: in order (both warps)
   uint64_t full[kN], empty[kN];
   uint64_t s_full[2];
   uint64_t p_full, o_done, o_free, drain;
@@ -51,7 +52,7 @@ struct Smem {
   static constexpr int ring = q + kQBytes;
   static constexpr int stage = ring + kN * fp4::kSlot;
   static constexpr int pt = stage + fp4::kStageBytes;
-  static constexpr int pt_bytes = NR * 256;  // [NR rows][128 tokens] f16
+  static constexpr int pt_bytes = NR * 256;  // [NR rows][128 tokens] bf16
   static constexpr int ctrl = pt + pt_bytes;
   static constexpr int rows = ctrl + 1024;
   static constexpr int total = rows + (int)sizeof(fp4::RowTable);
@@ -94,7 +95,8 @@ __global__ void __launch_bounds__(fp4::kThreads, 1)
   const int rows_here = p.rows;  // at most 64
 
   if (threadIdx.x == 0) {
-    mbar_init(&c->q_full, 1);
+    mbar_init(&c->q_raw, 1);
+    mbar_init(&c->q_full, 2);
     mbar_init(&c->q_empty, 1);
     for (int i = 0; i < kN; ++i) { mbar_init(&c->full[i], 4); mbar_init(&c->empty[i], 1); }
     for (int i = 0; i < 2; ++i) mbar_init(&c->s_full[i], 1);
@@ -128,19 +130,26 @@ __global__ void __launch_bounds__(fp4::kThreads, 1)
   Piece pc;
   auto wait = [&](uint64_t* bar, uint32_t parity) { return timed_wait(c, bar, parity, p); };
 
-  if (warp == 0) {
+  if (warp == 0 || warp == 2) {
     // ------------------------------------------------------------ Q
-    if (lane == 0) {
-      int pi = 0, q_issued = 0;
-      while (it.next(pc)) {
-        if (!timed_wait(c, &c->q_empty, (pi & 1) ^ 1, p)) break;
-        mbar_arrive_expect_tx(&c->q_full, kQBytes);
-        for (int j = 0; j < 9; ++j) tma_load_2d(sQ + j * 8192, &tm_q, &c->q_full, 64 * j, pc.unit * p.rows);
+    int pi = 0, q_issued = 0;
+    while (it.next(pc)) {
+      if (warp == 0 && lane == 0 && timed_wait(c, &c->q_empty, (pi & 1) ^ 1, p)) {
+        mbar_arrive_expect_tx(&c->q_raw, kQBytes);
+        for (int j = 0; j < 9; ++j) tma_load_2d(sQ + j * 8192, &tm_q, &c->q_raw, 64 * j, pc.unit * p.rows);
         ++q_issued;
-        ++pi;
       }
-      if (q_issued > 0) mbar_wait(&c->q_full, (uint32_t)((q_issued - 1) & 1), p.timeout_ns);
+      __syncwarp();
+      bool ok = true;
+      if (lane == 0) ok = timed_wait(c, &c->q_raw, pi & 1, p);
+      if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) break;
+      fp4::order_query_tile(sQ, lane + 16 * warp, 64);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&c->q_full);
+      ++pi;
     }
+    if (warp == 0 && lane == 0 && q_issued > 0) mbar_wait(&c->q_raw, (uint32_t)((q_issued - 1) & 1), p.timeout_ns);
     __syncwarp();
   } else if (warp == 3) {
     fp4::row_warp<false, SPARSE>(p, it, rt, lane, wait);
@@ -151,7 +160,7 @@ __global__ void __launch_bounds__(fp4::kThreads, 1)
     // ------------------------------------------------------------ MMA issuer: S(0), S(1), O(0), S(2), O(1), ...
     if (lane == 0) {
       const uint32_t idesc_s = idesc_bf16(64, 128, false, false);
-      const uint32_t idesc_o = idesc_f16(128, NR, true, false);
+      const uint32_t idesc_o = idesc_bf16(128, NR, true, false);
       // descriptors: Q, K slots and P^T are K-major, V slots MN-major (halves 8 KB apart)
       const uint32_t q_lo = sdesc_lo(smem_u32(sQ), 16), k_lo = sdesc_lo(smem_u32(sRing), 16);
       const uint32_t v_lo = sdesc_lo(smem_u32(sRing), 8192), p_lo = sdesc_lo(smem_u32(sP), 16);
@@ -249,6 +258,7 @@ __global__ void __launch_bounds__(fp4::kThreads, 1)
           };
           vmask = make_uint4(word(0), word(1), word(2), word(3));
         }
+        if (!rvalid) vmask = make_uint4(0, 0, 0, 0);
         if (!timed_wait(c, &c->s_full[b], (gt >> 1) & 1, p)) { stop = true; break; }
         tc_fence_after();
         const uint32_t s_addr = tmem + lane_base + kTmemS + 128 * b;
@@ -259,12 +269,10 @@ __global__ void __launch_bounds__(fp4::kThreads, 1)
           uint32_t sv[32];
           tmem_ld32(s_addr + 32 * w, sv);
           tmem_ld_wait();
-          const uint32_t mw = pick4u(vmask, w);
+          fp4::mask_scores(sv, pick4u(vmask, w));
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            tmax = fmaxf(tmax, ((mw >> i) & 1u) ? __uint_as_float(sv[i]) : -INFINITY);
+          for (int i = 0; i < 32; ++i) tmax = fmaxf(tmax, __uint_as_float(sv[i]));
         }
-        if (!rvalid) tmax = -INFINITY;
         float alpha = 1.f;
         int need = 0;
         if (tmax > m_used + thresh || (m_used == -INFINITY && tmax > -INFINITY)) {
@@ -274,7 +282,7 @@ __global__ void __launch_bounds__(fp4::kThreads, 1)
           m_used = m_new;
           l_sum *= alpha;
         }
-        // pass 2: probabilities (masked by select, never by branch) -> f16, staged
+        // pass 2: probabilities (a masked score is -inf: e^-inf = 0) -> bf16, staged
         // in TMEM over the S columns already read (tokens 32w.. -> columns 16w..)
         const float mc = (m_used == -INFINITY ? 0.f : m_used) * p.scale_log2;
         float part = 0.f;
@@ -283,15 +291,13 @@ __global__ void __launch_bounds__(fp4::kThreads, 1)
           uint32_t sv[32];
           tmem_ld32(s_addr + 32 * w, sv);
           tmem_ld_wait();
-          const uint32_t mw = rvalid ? pick4u(vmask, w) : 0u;
+          fp4::mask_scores(sv, pick4u(vmask, w));
           uint32_t pk[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const float e0 = ex2_approx(fmaf(__uint_as_float(sv[2 * i]), p.scale_log2, -mc));
-            const float e1 = ex2_approx(fmaf(__uint_as_float(sv[2 * i + 1]), p.scale_log2, -mc));
-            const float p0 = ((mw >> (2 * i)) & 1u) ? e0 : 0.f;
-            const float p1 = ((mw >> (2 * i + 1)) & 1u) ? e1 : 0.f;
-            pk[i] = pack_f16x2(p0, p1);
+            const float p0 = ex2_approx(fmaf(__uint_as_float(sv[2 * i]), p.scale_log2, -mc));
+            const float p1 = ex2_approx(fmaf(__uint_as_float(sv[2 * i + 1]), p.scale_log2, -mc));
+            pk[i] = pack_bf16x2(p0, p1);
             part += p0 + p1;
           }
           tmem_st16(s_addr + 16 * w, pk);
@@ -352,7 +358,7 @@ __global__ void __launch_bounds__(fp4::kThreads, 1)
       if (owner) {
         float inv = 0.f, lse = -INFINITY;
         if (l_sum > 0.f) {
-          inv = 1.f / l_sum;
+          inv = fp4::kOutScale / l_sum;
           lse = m_used * p.scale + logf(l_sum);
         }
         if (pc.single && rvalid && p.sink != nullptr) inv *= fold_sink(lse, p.sink[row_head(p, pc.unit, row0 + r)]);
@@ -366,7 +372,7 @@ __global__ void __launch_bounds__(fp4::kThreads, 1)
       if (!group_sync(c, &c->grp_sm, gph, p)) { stop = true; break; }
 #pragma unroll 1
       for (int m = 0; m < 4; ++m) {
-        const int d = 128 * m + 32 * q4 + lane;
+        const int d = 128 * m + 32 * q4 + (lane & 24) + fp4::element_of(lane & 7);
 #pragma unroll 1
         for (int c16 = 0; c16 < NR / 16; ++c16) {
           uint32_t ov[16];

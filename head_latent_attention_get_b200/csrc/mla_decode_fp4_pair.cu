@@ -5,16 +5,16 @@
 // Work split, TMEM layout and softmax are those of the bf16 pair kernel
 // (mla_decode_pair.cu): a step is two 128-token tiles; CTA r supplies K of
 // tile r and, for all 256 tokens, V of its value dims {256j + 128r + [0,128)}:
-//   S = Q K^T   pair MMA M=128 (64 rows per CTA) x N=256 tokens x K=576, bf16
-//   O = P V     pair MMA M=128 x N=256 value dims x K=256 tokens, twice, f16
+//   S = Q K^T   pair MMA M=128 (64 rows per CTA) x N=256 tokens x K=576
+//   O = P V     pair MMA M=128 x N=256 value dims x K=256 tokens, twice
 // Each CTA's eight converter warps fill its ring from the records
 // (mla_fp4.cuh) in the order in which the even CTA's MMA issuer consumes it.
 //
 // Warp roles (512 threads per CTA):
-//   0 Q via TMA (both CTAs; completion counted on the even CTA's barrier)
+//   0 Q via TMA, then 0 and 3 put it in the converted keys' order (both CTAs)
 //   1 TMEM allocation (both); MMA issue (even CTA); forwarding of the odd
 //     CTA's slot completions (odd CTA)
-//   2 cache rows   3 idle
+//   2 cache rows
 //   4-7 softmax + epilogue (both): thread i = (row i % 64, token half i / 64)
 //   8-15 converters
 // All waits are bounded; a timeout sets MLA_DEVICE_STATUS_TIMEOUT, raises the
@@ -37,11 +37,12 @@ constexpr float kRescaleLog2 = 8.0f;
 
 struct Ctrl {
   // barriers counted on the even CTA (the MMA issuer) ...
-  uint64_t q_full;                     // 1 arrival (+ both CTAs' Q bytes)
+  uint64_t q_full;                     // 4 arrivals: both CTAs' Q is in order
   uint64_t full[kN];                   // 8 converter warps + 1 forward from the odd CTA
   uint64_t p_full[2], o_free;          // 8 arrivals: 4 softmax warps x 2 CTAs
   uint64_t drain;
   // ... and in each CTA
+  uint64_t q_raw;                      // Q as loaded
   uint64_t q_empty, empty[kN];         // pair-MMA commits
   uint64_t s_full[2], o_done[2];       // pair-MMA commits; o_done[g & 1] completes O of step g
   uint64_t v_loc[kN];                  // odd CTA: its 8 converter warps
@@ -124,7 +125,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
   const int row0 = 64 * (int)pr.rank;   // first row of this CTA within a unit
 
   if (threadIdx.x == 0) {
-    mbar_init(&c->q_full, 1);
+    mbar_init(&c->q_full, 4);
+    mbar_init(&c->q_raw, 1);
     for (int i = 0; i < kN; ++i) mbar_init(&c->full[i], 4 + 1);
     for (int i = 0; i < 2; ++i) mbar_init(&c->p_full[i], 8);
     mbar_init(&c->o_free, 8);
@@ -158,22 +160,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
   Piece pc;
   auto wait = [&](uint64_t* bar, uint32_t parity) { return pwait(pr, bar, parity, p); };
 
-  if (warp == 0) {
+  if (warp == 0 || warp == 3) {
     // ------------------------------------------------------------ Q
-    if (lane == 0) {
-      int pi = 0, q_issued = 0;
-      while (it.next(pc)) {
-        if (!pwait(pr, &c->q_empty, (pi & 1) ^ 1, p)) break;
-        const uint32_t qbar = map_to_rank(smem_u32(&c->q_full), 0);
-        if (pr.leader) mbar_arrive_expect_tx(&c->q_full, 2 * kQBytes);
-        const int qy = pc.unit * p.rows + row0;
-        for (int j = 0; j < 9; ++j) tma_load_2d_pair(sQ + j * 8192, &tm_q, qbar, 64 * j, qy);
+    int pi = 0, q_issued = 0;
+    while (it.next(pc)) {
+      if (warp == 0 && lane == 0 && pwait(pr, &c->q_empty, (pi & 1) ^ 1, p)) {
+        mbar_arrive_expect_tx(&c->q_raw, kQBytes);
+        for (int j = 0; j < 9; ++j) tma_load_2d(sQ + j * 8192, &tm_q, &c->q_raw, 64 * j, pc.unit * p.rows + row0);
         ++q_issued;
-        ++pi;
       }
-      // the even CTA's barrier counts both CTAs' copies
-      if (pr.leader && q_issued > 0) mbar_wait_cluster(&c->q_full, (uint32_t)((q_issued - 1) & 1), p.timeout_ns);
+      __syncwarp();
+      bool ok = true;
+      if (lane == 0) ok = pwait(pr, &c->q_raw, pi & 1, p);
+      if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) break;
+      fp4::order_query_tile(sQ, lane + (warp == 0 ? 0 : 32), 64);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) arrive_leader(pr, &c->q_full);
+      ++pi;
     }
+    if (warp == 0 && lane == 0 && q_issued > 0) mbar_wait(&c->q_raw, (uint32_t)((q_issued - 1) & 1), p.timeout_ns);
     __syncwarp();
   } else if (warp == 2) {
     fp4::row_warp<true, SPARSE>(p, it, rt, lane, wait);
@@ -200,7 +206,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer: S(0), S(1), O(0), S(2), O(1), ...
     const uint32_t idesc_s = idesc_bf16(128, 256, false, false);
-    const uint32_t idesc_o = idesc_f16(128, 256, false, true);
+    const uint32_t idesc_o = idesc_bf16(128, 256, false, true);
     // descriptors: Q, K slots and P are K-major, V slots MN-major (halves 8 KB apart)
     const uint32_t q_lo = sdesc_lo(smem_u32(sQ), 16), k_lo = sdesc_lo(smem_u32(sRing), 16);
     const uint32_t v_lo = sdesc_lo(smem_u32(sRing), 8192), p_lo = sdesc_lo(smem_u32(sP), 16);
@@ -309,9 +315,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
           uint32_t sv[32];
           tmem_ld32(s_addr + 32 * w, sv);
           tmem_ld_wait();
-          const uint32_t mw = pick4u(vm, w);
+          fp4::mask_scores(sv, pick4u(vm, w));
 #pragma unroll
-          for (int i = 0; i < 32; ++i) tmax = fmaxf(tmax, ((mw >> i) & 1u) ? __uint_as_float(sv[i]) : -INFINITY);
+          for (int i = 0; i < 32; ++i) tmax = fmaxf(tmax, __uint_as_float(sv[i]));
         }
         c->mx[gt & 1][half][row] = tmax;
         if (!group_sync(pr, gph, p)) { stop = true; break; }
@@ -325,7 +331,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
           m_used = tmax;
           l_sum *= alpha;
         }
-        // pass 2: probabilities (masked by select) -> f16 -> the P buffer,
+        // pass 2: probabilities (a masked score is -inf: e^-inf = 0) -> bf16 -> the P buffer,
         // K-major [64 rows][64 keys] per slice: keys 64s.. in slice s; this
         // thread's keys are 128*half + [0,128), slices 2*half and 2*half + 1.
         // The single P buffer was last read by the O product of step gt - 1,
@@ -339,14 +345,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
           uint32_t sv[32];
           tmem_ld32(s_addr + 32 * w, sv);
           tmem_ld_wait();
-          const uint32_t mw = pick4u(vm, w);
+          fp4::mask_scores(sv, pick4u(vm, w));
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const float e0 = ex2_approx(fmaf(__uint_as_float(sv[2 * i]), p.scale_log2, -mc));
-            const float e1 = ex2_approx(fmaf(__uint_as_float(sv[2 * i + 1]), p.scale_log2, -mc));
-            const float p0 = ((mw >> (2 * i)) & 1u) ? e0 : 0.f;
-            const float p1 = ((mw >> (2 * i + 1)) & 1u) ? e1 : 0.f;
-            pk[i] = pack_f16x2(p0, p1);
+            const float p0 = ex2_approx(fmaf(__uint_as_float(sv[2 * i]), p.scale_log2, -mc));
+            const float p1 = ex2_approx(fmaf(__uint_as_float(sv[2 * i + 1]), p.scale_log2, -mc));
+            pk[i] = pack_bf16x2(p0, p1);
             part += p0 + p1;
           }
         };
@@ -399,7 +403,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
       tc_fence_after();
       float inv = 0.f, lse = -INFINITY;
       if (l_tot > 0.f) {
-        inv = 1.f / l_tot;
+        inv = fp4::kOutScale / l_tot;
         lse = m_used * p.scale + logf(l_tot);
       }
       if (pc.single && rvalid && p.sink != nullptr) inv *= fold_sink(lse, p.sink[row_head(p, pc.unit, grow)]);
@@ -408,6 +412,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
         if (pc.single) p.lse[orow] = lse;
         else p.ws_lse[(size_t)pc.ws_idx * p.rows + grow] = lse;
       }
+      // column of value dim i among 16 columns (the converted order of each group of 8)
+      auto position = [](int i) { return (i & 8) | ((i & 3) << 1) | ((i >> 2) & 1); };
 #pragma unroll 1
       for (int jd = 0; jd < 2; ++jd) {
         const int d0 = 256 * jd + 128 * half;
@@ -421,7 +427,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
               uint32_t pk[8];
 #pragma unroll
               for (int i = 0; i < 8; ++i)
-                pk[i] = pack_bf16x2(__uint_as_float(ov[2 * i]) * inv, __uint_as_float(ov[2 * i + 1]) * inv);
+                pk[i] = pack_bf16x2(__uint_as_float(ov[position(2 * i)]) * inv, __uint_as_float(ov[position(2 * i + 1)]) * inv);
               uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + orow * kDv + d0 + 16 * c16);
               dst[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
               dst[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
@@ -429,8 +435,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
               float4* dst = reinterpret_cast<float4*>(p.ws_o + ((size_t)pc.ws_idx * p.rows + grow) * kDv + d0 + 16 * c16);
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                dst[i] = make_float4(__uint_as_float(ov[4 * i]) * inv, __uint_as_float(ov[4 * i + 1]) * inv,
-                                     __uint_as_float(ov[4 * i + 2]) * inv, __uint_as_float(ov[4 * i + 3]) * inv);
+                dst[i] = make_float4(__uint_as_float(ov[position(4 * i)]) * inv, __uint_as_float(ov[position(4 * i + 1)]) * inv,
+                                     __uint_as_float(ov[position(4 * i + 2)]) * inv,
+                                     __uint_as_float(ov[position(4 * i + 3)]) * inv);
             }
           }
         }
@@ -442,14 +449,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
   }
 
   // ---------------------------------------------------------------- teardown
-  // In a normal exit every copy has landed: the MMA issuer consumed each Q
-  // phase, and the converters waited for their own copies. After an abort (a
-  // bounded wait ran out) a Q copy of the odd CTA may still be in flight, and
-  // its completion is counted on the even CTA's barrier, where no wait here
-  // observes it. Such copies land within microseconds, so the CTA holds its
-  // shared memory for a fixed 200 us of wall time (%globaltimer, not a sleep hint that may
-  // return early) before the final cluster barrier; this bounds the window,
-  // it does not prove every copy landed.
+  // Every copy of this CTA has landed: the converters and the Q warp waited
+  // for their own. After an abort a remote arrive or a pair MMA of the other
+  // CTA may be pending for microseconds, so the CTA holds its shared memory
+  // for a fixed 200 us of wall time (%globaltimer, not a sleep hint that may
+  // return early) before the final cluster barrier.
   if (aborted(pr)) {
     const uint64_t t0 = global_timer_ns();
     while (global_timer_ns() - t0 < 200000) {

@@ -4,10 +4,20 @@
 // token records into tensor-core operands.
 //
 // A record is 256 bytes of E2M1 pairs, 32 UE4M3 scales (one per 16 latent
-// values) and 64 bf16 RoPE dims. K takes bf16 (the query's type: one MMA wants
-// one type for both operands), V takes f16 (the probabilities are written in
-// f16 too). Both are exact: an E2M1 x UE4M3 product has at most 6 significant
-// bits and lies in [2^-10, 2688].
+// values) and 64 bf16 RoPE dims. Latent values become bf16 without rounding:
+// an E2M1 x UE4M3 product has at most 6 significant bits.
+//
+// Conversion: a nibble's three magnitude bits, put where a bf16 has the two
+// low exponent bits and the top mantissa bit, read as its value times 2^-126
+// (exponent field 0 is the subnormal 0.5); one multiplication by scale * 2^119
+// gives value * 2^-7 and the sign bit is moved along, five instructions for
+// two values. The 2^7 is put back in the query (K) and the output (V). Both
+// halves of a 32-bit word are worked on at once, so the eight values of a word
+// come out as elements 0 4 1 5 2 6 3 7: the query is put in the same order
+// before its first use, and the output is written back in order.
+// The five instructions bound the kernels: 142 clk of a 16 KB slot's ~256 clk
+// of MMA time for eight warps alone on an SM, against 197 for byte-permute
+// tables and 131 for the hardware conversion to f16, whose type Q lacks.
 //
 // A converter thread stages the 16 code bytes of its next eight slots in shared
 // memory of its own (cp.async, no other thread touches them): slot i of a
@@ -16,6 +26,7 @@
 // one phase ahead. Reading the codes again for V costs 256 bytes a token from
 // L2, a quarter of the bf16 cache's V re-read.
 #pragma once
+#include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include "mla_decode_util.cuh"
@@ -86,25 +97,12 @@ __device__ __forceinline__ uint4 ldg16(const uint8_t* p) {
 }
 
 // ---------------------------------------------------------------- conversions
-// Eight E2M1 codes (one word, element i in nibble i) -> 8 bf16 times a scale.
-// The magnitudes' bf16 high and low bytes come from byte permutes that use
-// the nibbles themselves as selectors; the sign bytes from permutes in their
-// sign-replicating form. (The hardware conversion gives f16, and f16 -> bf16
-// would cost three more instructions per pair.)
-__device__ __forceinline__ uint4 e2m1x8_to_bf16(uint32_t w, __nv_bfloat162 s) {
-  const uint32_t m = w & 0x77777777u, wl = w << 4;
-  uint32_t o[4];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t sel = m >> (16 * i);
-    uint32_t sign, hi, lo;
-    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(sign) : "r"(wl), "r"(w), "r"(i == 0 ? 0xD9C8u : 0xFBEAu));
-    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(hi) : "r"(0x3F3F3F00u), "r"(0x40404040u), "r"(sel));
-    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(lo) : "r"(0xC0800000u), "r"(0xC0804000u), "r"(sel));
-    hi |= sign & 0x80808080u;
-    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(o[2 * i]) : "r"(lo), "r"(hi), "r"(0x5140u));
-    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(o[2 * i + 1]) : "r"(lo), "r"(hi), "r"(0x7362u));
-  }
+// Eight E2M1 codes (one word, element i in nibble i) times a scale -> 8 bf16 in
+// element order 0 4 1 5 2 6 3 7. s: the scale * 2^119, twice.
+__device__ __forceinline__ uint4 e2m1x8(uint32_t w, __nv_bfloat162 s) {
+  constexpr uint32_t kSign = 0x80008000u, kMag = 0x01C001C0u;
+  uint32_t o[4] = {((w << 12) & kSign) | ((w << 6) & kMag), ((w << 8) & kSign) | ((w << 2) & kMag),
+                   ((w << 4) & kSign) | ((w >> 2) & kMag), (w & kSign) | ((w >> 6) & kMag)};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const __nv_bfloat162 v = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&o[i]), s);
@@ -112,42 +110,55 @@ __device__ __forceinline__ uint4 e2m1x8_to_bf16(uint32_t w, __nv_bfloat162 s) {
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
-// The same in f16, by the hardware conversion of a byte into two f16.
-__device__ __forceinline__ uint4 e2m1x8_to_f16(uint32_t w, __half2 s) {
-  uint32_t o[4];
+// Position within an 8-element group -> element.
+__device__ __forceinline__ int element_of(int pos) { return (pos >> 1) | ((pos & 1) << 2); }
+// A 16-byte chunk of the query: times 2^7, in the converted keys' order.
+__device__ __forceinline__ uint4 order_query(uint4 v) {
+  const __nv_bfloat162 f = __float2bfloat162_rn(128.f);
+  uint32_t o[4] = {__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
+                   __byte_perm(v.y, v.w, 0x7632)};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __half2_raw hr = __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)((w >> (8 * i)) & 0xFFu), __NV_E2M1);
-    const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&hr), s);
-    o[i] = *reinterpret_cast<const uint32_t*>(&v);
+    const __nv_bfloat162 t = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&o[i]), f);
+    o[i] = *reinterpret_cast<const uint32_t*>(&t);
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
-// Two UE4M3 scale bytes (bit 7 ignored) as f16.
-__device__ __forceinline__ __half2 ue4m3x2(uint32_t s) {
-  const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(s & 0x7F7Fu), __NV_E4M3);
-  return *reinterpret_cast<const __half2*>(&hr);
+constexpr float kOutScale = 128.f;  // what the converted V lacks
+
+// Puts the latent slices of a query tile (64 rows) in order: thread t of `n`.
+__device__ __forceinline__ void order_query_tile(uint8_t* q, int t, int n) {
+#pragma unroll 4
+  for (int i = t; i < 8 * 512; i += n) {  // chunk order within a slice does not matter
+    uint4* c = reinterpret_cast<uint4*>(q) + i;
+    *c = order_query(*c);
+  }
 }
 
-// 32 codes and their two scale bytes as chunks c0..c0+3 of 128-byte row `row` of a swizzled tile.
-template <bool K>
+// 32 codes and their two UE4M3 scale bytes (bit 7 ignored) -> chunks c0..c0+3
+// of 128-byte row `row` of a swizzled tile.
 __device__ __forceinline__ void store_item(uint4 codes, uint32_t scales, uint8_t* tile, int row, int c0) {
-  const __half2 sc = ue4m3x2(scales);
+  const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(scales & 0x7F7Fu), __NV_E4M3);
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hr));
+  const __nv_bfloat162 s0 = __float2bfloat162_rn(f.x * 0x1p119f), s1 = __float2bfloat162_rn(f.y * 0x1p119f);
   const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __half s1 = i < 2 ? __low2half(sc) : __high2half(sc);
-    uint4 v;
-    if (K) v = e2m1x8_to_bf16(w[i], __bfloat162bfloat162(__float2bfloat16_rn(__half2float(s1))));
-    else v = e2m1x8_to_f16(w[i], __half2half2(s1));
-    *reinterpret_cast<uint4*>(sw128(tile, row, c0 + i)) = v;
-  }
+  for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(sw128(tile, row, c0 + i)) = e2m1x8(w[i], i < 2 ? s0 : s1);
 }
 // Copies a loaded word with an instruction that the compiler keeps where it is.
 __device__ __forceinline__ uint32_t settle(uint32_t a) {
   uint32_t b;
   asm volatile("mov.b32 %0, %1;" : "=r"(b) : "r"(a));
   return b;
+}
+
+// Scores of 32 keys: those whose bit of `valid` is clear become -inf. Most
+// words are full and cost one comparison.
+__device__ __forceinline__ void mask_scores(uint32_t (&sv)[32], uint32_t valid) {
+  if (valid == 0xffffffffu) return;
+#pragma unroll
+  for (int i = 0; i < 32; ++i)
+    if (!((valid >> i) & 1u)) sv[i] = 0xff800000u;
 }
 
 // ---------------------------------------------------------------- row warp
@@ -295,8 +306,8 @@ __device__ __forceinline__ void convert_ring(const DecodeParams& p, const PieceI
       uint8_t* s = ring + slot * kSlot;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        if (k) store_item<true>(codes[j], sc[0][j], s, ktok + 16 * j, 4 * khalf);
-        else store_item<false>(codes[j], sc[0][j], s + (vq >> 1) * 8192, vtok + 8 * j, 4 * (vq & 1));
+        store_item(codes[j], sc[0][j], s + (k ? 0 : (vq >> 1) * 8192), k ? ktok + 16 * j : vtok + 8 * j,
+                   4 * (k ? khalf : vq & 1));
       }
       fence_proxy_async_smem();
       __syncwarp();

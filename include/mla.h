@@ -98,7 +98,7 @@ enum {
    *   [288,416) 64 bf16 RoPE dims
    * value = e2m1 * ue4m3 (bit 7 of a scale byte is ignored), used exactly;
    * the RoPE dims are used as stored. The query is bf16, 576 values. Paged
-   * and token-sparse decoding; the probabilities are rounded to f16. */
+   * and token-sparse decoding. */
   MLA_KV_FP4_E2M1 = 3
 };
 

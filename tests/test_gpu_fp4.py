@@ -1,8 +1,7 @@
 """GPU parity of decoding over 4-bit token records (MLA_KV_FP4_E2M1), paged and
 token-sparse, on both kernels (units of at most 64 rows, and of 65-128 rows),
 against the fp64 oracle. The tolerances are the bf16 path's (gpu_helpers):
-scores are the same bf16 products, and the probabilities are rounded to f16,
-which is finer than bf16."""
+the stored values are exact in bf16, so the arithmetic is the same."""
 import dataclasses
 
 import numpy as np
