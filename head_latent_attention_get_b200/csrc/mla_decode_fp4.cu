@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(fp4::kThreads, 1)
   Ctrl* c = reinterpret_cast<Ctrl*>(smem + L::ctrl);
   fp4::RowTable* rt = reinterpret_cast<fp4::RowTable*>(smem + L::rows);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp: known to be uniform
   const int part = blockIdx.x, row0 = 0;
   const int rows_here = p.rows;  // at most 64
 
@@ -158,14 +158,15 @@ __global__ void __launch_bounds__(fp4::kThreads, 1)
                              [&](int slot) { return &c->full[slot]; });
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer: S(0), S(1), O(0), S(2), O(1), ...
-    if (lane == 0) {
+    if (elect_one()) {
       const uint32_t idesc_s = idesc_bf16(64, 128, false, false);
       const uint32_t idesc_o = idesc_bf16(128, NR, true, false);
       // descriptors: Q, K slots and P^T are K-major, V slots MN-major (halves 8 KB apart)
       const uint32_t q_lo = sdesc_lo(smem_u32(sQ), 16), k_lo = sdesc_lo(smem_u32(sRing), 16);
       const uint32_t v_lo = sdesc_lo(smem_u32(sRing), 8192), p_lo = sdesc_lo(smem_u32(sP), 16);
       constexpr uint32_t d_hi = sdesc_hi(1024);
-      int sc = 0, gs = 0, go = 0, pi = 0;
+      int gs = 0, go = 0, pi = 0;
+      fp4::RingPos<kN> pos;
       bool stop = false;
       while (!stop && it.next(pc)) {
         if (!timed_wait(c, &c->q_full, pi & 1, p)) break;
@@ -177,9 +178,9 @@ __global__ void __launch_bounds__(fp4::kThreads, 1)
             // S buffer b was last read by the softmax of tile gs - 2, whose
             // P the O product of that tile (issued before) waited for
             const uint32_t d = tmem + kTmemS + 128 * (gs & 1);
-            for (int j = 0; j < 9; ++j, ++sc) {
-              const int slot = sc % kN;
-              if (!timed_wait(c, &c->full[slot], (sc / kN) & 1, p)) { stop = true; break; }
+            for (int j = 0; j < 9; ++j, pos.advance()) {
+              const int slot = pos.slot;
+              if (!timed_wait(c, &c->full[slot], pos.parity, p)) { stop = true; break; }
               tc_fence_after();
               const uint32_t qa = q_lo + j * (8192 >> 4), kb = k_lo + slot * (fp4::kSlot >> 4);
 #pragma unroll
@@ -196,9 +197,9 @@ __global__ void __launch_bounds__(fp4::kThreads, 1)
             const bool first = g == 0;
             if (first && pi > 0 && !timed_wait(c, &c->o_free, (pi - 1) & 1, p)) { stop = true; break; }
             if (!timed_wait(c, &c->p_full, go & 1, p)) { stop = true; break; }
-            for (int j = 0; j < 8; ++j, ++sc) {  // value dims 128 (j / 2) .., token half j % 2
-              const int slot = sc % kN, m = j >> 1, hf = j & 1;
-              if (!timed_wait(c, &c->full[slot], (sc / kN) & 1, p)) { stop = true; break; }
+            for (int j = 0; j < 8; ++j, pos.advance()) {  // value dims 128 (j / 2) .., token half j % 2
+              const int slot = pos.slot, m = j >> 1, hf = j & 1;
+              if (!timed_wait(c, &c->full[slot], pos.parity, p)) { stop = true; break; }
               tc_fence_after();
               const uint32_t va = v_lo + slot * (fp4::kSlot >> 4), pa = p_lo + hf * (NR * 128 >> 4);
 #pragma unroll

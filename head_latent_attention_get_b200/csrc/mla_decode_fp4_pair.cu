@@ -115,7 +115,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
   Ctrl* c = reinterpret_cast<Ctrl*>(smem + Smem::ctrl);
   fp4::RowTable* rt = reinterpret_cast<fp4::RowTable*>(smem + Smem::rows);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp: known to be uniform
   Pair pr;
   pr.rank = cluster_rank();
   pr.leader = pr.rank == 0;
@@ -211,9 +211,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
     const uint32_t q_lo = sdesc_lo(smem_u32(sQ), 16), k_lo = sdesc_lo(smem_u32(sRing), 16);
     const uint32_t v_lo = sdesc_lo(smem_u32(sRing), 8192), p_lo = sdesc_lo(smem_u32(sP), 16);
     constexpr uint32_t d_hi = sdesc_hi(1024);
-    int sc = 0, gs = 0, go = 0, pi = 0;
+    int gs = 0, go = 0, pi = 0;
+    fp4::RingPos<kN> pos;
     bool stop = false;
-    if (lane == 0) {
+    if (elect_one()) {
       while (!stop && it.next(pc)) {
         if (!pwait(pr, &c->q_full, pi & 1, p)) { stop = true; break; }
         const int nsteps = fp4::steps_of<true>(pc);
@@ -226,9 +227,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
             const int b = gs & 1;
             tc_fence_after();
             const uint32_t d = tmem + kTmemS + 128 * b;
-            for (int j = 0; j < 9; ++j, ++sc) {
-              const int slot = sc % kN;
-              if (!pwait(pr, &c->full[slot], (sc / kN) & 1, p)) { stop = true; break; }
+            for (int j = 0; j < 9; ++j, pos.advance()) {
+              const int slot = pos.slot;
+              if (!pwait(pr, &c->full[slot], pos.parity, p)) { stop = true; break; }
               tc_fence_after();
               const uint32_t qa = q_lo + j * (8192 >> 4), kb = k_lo + slot * (fp4::kSlot >> 4);
 #pragma unroll
@@ -246,9 +247,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
             if (first && pi > 0 && !pwait(pr, &c->o_free, (pi - 1) & 1, p)) { stop = true; break; }
             if (!pwait(pr, &c->p_full[go & 1], (go >> 1) & 1, p)) { stop = true; break; }
             for (int q = 0; q < 4 && !stop; ++q) {
-              for (int jd = 0; jd < 2; ++jd, ++sc) {
-                const int slot = sc % kN;
-                if (!pwait(pr, &c->full[slot], (sc / kN) & 1, p)) { stop = true; break; }
+              for (int jd = 0; jd < 2; ++jd, pos.advance()) {
+                const int slot = pos.slot;
+                if (!pwait(pr, &c->full[slot], pos.parity, p)) { stop = true; break; }
                 tc_fence_after();
                 const uint32_t va = v_lo + slot * (fp4::kSlot >> 4), pa = p_lo + q * (8192 >> 4);
 #pragma unroll

@@ -87,6 +87,20 @@ struct RowTable {
   uint32_t valid[kRowDepth][8];
 };
 
+// Position in the ring: slot and the parity of its current use.
+template <int N>
+struct RingPos {
+  int slot = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void advance(int n = 1) {
+    slot += n;
+    if (slot >= N) {
+      slot -= N;
+      parity ^= 1u;
+    }
+  }
+};
+
 // 16 bytes that are read once per CTA and ring: no L1 line is kept for them.
 __device__ __forceinline__ uint4 ldg16(const uint8_t* p) {
   uint4 v;
