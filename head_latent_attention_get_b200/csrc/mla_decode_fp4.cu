@@ -6,7 +6,7 @@
 //   S    = Q K^T     tcgen05 M=64 rows x N=128 tokens x K=576
 //   softmax          one thread per query row, online, O rescaled lazily
 //   O^T += V^T P^T   tcgen05 M=128 value dims (4 chunks) x N=rows x K=128
-// The keys reach the tensor core through one ring of 16 KB slots that eight
+// The keys reach the tensor core through one ring of 32 KB entries that eight
 // converter warps fill from the records (mla_fp4.cuh), in the order in which
 // the one MMA issuer consumes it: S(0), S(1), O(0), S(2), O(1), ...
 //
@@ -26,7 +26,7 @@
 namespace mla {
 namespace {
 
-constexpr int kN = 6;                  // ring slots of 16 KB
+using fp4::kN;
 constexpr int kQBytes = 9 * 8192;      // 64 rows x 576 dims
 constexpr int kTmemCols = 512;
 constexpr int kTmemS = 256;            // S buffers at columns 256 and 384
@@ -154,39 +154,41 @@ __global__ void __launch_bounds__(fp4::kThreads, 1)
   } else if (warp == 3) {
     fp4::row_warp<false, SPARSE>(p, it, rt, lane, wait);
   } else if (warp >= 8) {
-    fp4::convert_ring<false, kN>(p, it, rt, sRing, sStage, c->empty, warp - 8, lane, 0, wait,
+    fp4::convert_ring<false>(p, it, rt, sRing, sStage, c->empty, warp - 8, lane, 0, wait,
                              [&](int slot) { return &c->full[slot]; });
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer: S(0), S(1), O(0), S(2), O(1), ...
     if (elect_one()) {
       const uint32_t idesc_s = idesc_bf16(64, 128, false, false);
       const uint32_t idesc_o = idesc_bf16(128, NR, true, false);
-      // descriptors: Q, K slots and P^T are K-major, V slots MN-major (halves 8 KB apart)
+      // descriptors: Q, K and P^T are K-major, V is MN-major (slices 16 KB apart)
       const uint32_t q_lo = sdesc_lo(smem_u32(sQ), 16), k_lo = sdesc_lo(smem_u32(sRing), 16);
-      const uint32_t v_lo = sdesc_lo(smem_u32(sRing), 8192), p_lo = sdesc_lo(smem_u32(sP), 16);
+      const uint32_t v_lo = sdesc_lo(smem_u32(sRing), fp4::kSlice), p_lo = sdesc_lo(smem_u32(sP), 16);
       constexpr uint32_t d_hi = sdesc_hi(1024);
       int gs = 0, go = 0, pi = 0;
-      fp4::RingPos<kN> pos;
+      fp4::RingPos pos;
       bool stop = false;
       while (!stop && it.next(pc)) {
         if (!timed_wait(c, &c->q_full, pi & 1, p)) break;
         const int nsteps = fp4::steps_of<false>(pc);
         for (int h = 0; h <= 2 * nsteps && !stop; ++h) {
-          if (!fp4::entry_exists(h, nsteps)) continue;
-          const int g = fp4::entry_step(h);
-          if (fp4::entry_is_k(h)) {
+          if (!fp4::phase_exists(h, nsteps)) continue;
+          const int g = fp4::phase_step(h);
+          if (fp4::phase_is_k(h)) {
             // S buffer b was last read by the softmax of tile gs - 2, whose
             // P the O product of that tile (issued before) waited for
             const uint32_t d = tmem + kTmemS + 128 * (gs & 1);
-            for (int j = 0; j < 9; ++j, pos.advance()) {
+            for (int e = 0; e < 5; ++e, pos.advance()) {  // four latent entries of two slices, then RoPE
               const int slot = pos.slot;
               if (!timed_wait(c, &c->full[slot], pos.parity, p)) { stop = true; break; }
               tc_fence_after();
-              const uint32_t qa = q_lo + j * (8192 >> 4), kb = k_lo + slot * (fp4::kSlot >> 4);
+              const uint32_t qa = q_lo + 2 * e * (8192 >> 4), kb = k_lo + slot * (fp4::kSlot >> 4);
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                mma_bf16_ss(d, sdesc_join(qa + kk * 2, d_hi), sdesc_join(kb + kk * 2, d_hi), idesc_s,
-                            (j | kk) != 0 ? 1u : 0u);
+              for (int kk = 0; kk < 8; ++kk)
+                if (kk < 4 || e < 4)
+                  mma_bf16_ss(d, sdesc_join(qa + (kk >> 2) * (8192 >> 4) + (kk & 3) * 2, d_hi),
+                              sdesc_join(kb + (kk >> 2) * (fp4::kSlice >> 4) + (kk & 3) * 2, d_hi), idesc_s,
+                              (e | kk) != 0 ? 1u : 0u);
               mma_commit(&c->empty[slot]);
             }
             if (stop) break;
@@ -197,15 +199,16 @@ __global__ void __launch_bounds__(fp4::kThreads, 1)
             const bool first = g == 0;
             if (first && pi > 0 && !timed_wait(c, &c->o_free, (pi - 1) & 1, p)) { stop = true; break; }
             if (!timed_wait(c, &c->p_full, go & 1, p)) { stop = true; break; }
-            for (int j = 0; j < 8; ++j, pos.advance()) {  // value dims 128 (j / 2) .., token half j % 2
-              const int slot = pos.slot, m = j >> 1, hf = j & 1;
+            for (int m = 0; m < 4; ++m, pos.advance()) {  // value dims 128 m ..
+              const int slot = pos.slot;
               if (!timed_wait(c, &c->full[slot], pos.parity, p)) { stop = true; break; }
               tc_fence_after();
-              const uint32_t va = v_lo + slot * (fp4::kSlot >> 4), pa = p_lo + hf * (NR * 128 >> 4);
+              const uint32_t va = v_lo + slot * (fp4::kSlot >> 4);
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                mma_bf16_ss(tmem + 64 * m, sdesc_join(va + kk * (2048 >> 4), d_hi), sdesc_join(pa + kk * 2, d_hi), idesc_o,
-                            (first && hf == 0 && kk == 0) ? 0u : 1u);
+              for (int kk = 0; kk < 8; ++kk)
+                mma_bf16_ss(tmem + 64 * m, sdesc_join(va + kk * (2048 >> 4), d_hi),
+                            sdesc_join(p_lo + (kk >> 2) * (NR * 128 >> 4) + (kk & 3) * 2, d_hi), idesc_o,
+                            (first && kk == 0) ? 0u : 1u);
               mma_commit(&c->empty[slot]);
             }
             if (stop) break;

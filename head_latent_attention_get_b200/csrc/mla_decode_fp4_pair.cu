@@ -28,7 +28,7 @@
 namespace mla {
 namespace fp4pair {
 
-constexpr int kN = 5;                // ring slots of 16 KB
+using fp4::kN;
 constexpr int kQBytes = 9 * 8192;    // 64 rows x 576 dims
 constexpr int kPBytes = 4 * 8192;    // 64 rows x 256 tokens (one buffer)
 constexpr int kTmemCols = 512;
@@ -184,7 +184,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
   } else if (warp == 2) {
     fp4::row_warp<true, SPARSE>(p, it, rt, lane, wait);
   } else if (warp >= 8) {
-    fp4::convert_ring<true, kN>(p, it, rt, sRing, sStage, c->empty, warp - 8, lane, (int)pr.rank, wait,
+    fp4::convert_ring<true>(p, it, rt, sRing, sStage, c->empty, warp - 8, lane, (int)pr.rank, wait,
                             [&](int slot) { return pr.leader ? &c->full[slot] : &c->v_loc[slot]; });
   } else if (warp == 1 && !pr.leader) {
     // ------------------------------------------------------------ odd CTA: forward slot completions
@@ -192,7 +192,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
       int sc = 0;
       bool stop = false;
       while (!stop && it.next(pc)) {
-        const int nslots = 17 * fp4::steps_of<true>(pc);  // 9 K and 8 V slots per step
+        const int nslots = 9 * fp4::steps_of<true>(pc);  // 5 K and 4 V entries per step
         for (int i = 0; i < nslots; ++i, ++sc) {
           if (!pwait(pr, &c->v_loc[sc % kN], (sc / kN) & 1, p)) { stop = true; break; }
           // relaxed: a release arrive would wait for memory operations that
@@ -207,35 +207,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
     // ------------------------------------------------------------ MMA issuer: S(0), S(1), O(0), S(2), O(1), ...
     const uint32_t idesc_s = idesc_bf16(128, 256, false, false);
     const uint32_t idesc_o = idesc_bf16(128, 256, false, true);
-    // descriptors: Q, K slots and P are K-major, V slots MN-major (halves 8 KB apart)
+    // descriptors: Q, K and P are K-major, V is MN-major (slices 16 KB apart)
     const uint32_t q_lo = sdesc_lo(smem_u32(sQ), 16), k_lo = sdesc_lo(smem_u32(sRing), 16);
-    const uint32_t v_lo = sdesc_lo(smem_u32(sRing), 8192), p_lo = sdesc_lo(smem_u32(sP), 16);
+    const uint32_t v_lo = sdesc_lo(smem_u32(sRing), fp4::kSlice), p_lo = sdesc_lo(smem_u32(sP), 16);
     constexpr uint32_t d_hi = sdesc_hi(1024);
     int gs = 0, go = 0, pi = 0;
-    fp4::RingPos<kN> pos;
+    fp4::RingPos pos;
     bool stop = false;
     if (elect_one()) {
       while (!stop && it.next(pc)) {
         if (!pwait(pr, &c->q_full, pi & 1, p)) { stop = true; break; }
         const int nsteps = fp4::steps_of<true>(pc);
         for (int h = 0; h <= 2 * nsteps && !stop; ++h) {
-          if (!fp4::entry_exists(h, nsteps)) continue;
-          const int g = fp4::entry_step(h);
-          if (fp4::entry_is_k(h)) {
+          if (!fp4::phase_exists(h, nsteps)) continue;
+          const int g = fp4::phase_step(h);
+          if (fp4::phase_is_k(h)) {
             // S buffer b was last read by the softmax of step gs - 2, whose
             // P the O product of step gs - 2 (issued just before) waited for
             const int b = gs & 1;
             tc_fence_after();
             const uint32_t d = tmem + kTmemS + 128 * b;
-            for (int j = 0; j < 9; ++j, pos.advance()) {
+            for (int e = 0; e < 5; ++e, pos.advance()) {  // four latent entries of two slices, then RoPE
               const int slot = pos.slot;
               if (!pwait(pr, &c->full[slot], pos.parity, p)) { stop = true; break; }
               tc_fence_after();
-              const uint32_t qa = q_lo + j * (8192 >> 4), kb = k_lo + slot * (fp4::kSlot >> 4);
+              const uint32_t qa = q_lo + 2 * e * (8192 >> 4), kb = k_lo + slot * (fp4::kSlot >> 4);
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                mma_bf16_ss_pair(d, sdesc_join(qa + kk * 2, d_hi), sdesc_join(kb + kk * 2, d_hi), idesc_s,
-                                 (j | kk) != 0 ? 1u : 0u);
+              for (int kk = 0; kk < 8; ++kk)
+                if (kk < 4 || e < 4)
+                  mma_bf16_ss_pair(d, sdesc_join(qa + (kk >> 2) * (8192 >> 4) + (kk & 3) * 2, d_hi),
+                                   sdesc_join(kb + (kk >> 2) * (fp4::kSlice >> 4) + (kk & 3) * 2, d_hi), idesc_s,
+                                   (e | kk) != 0 ? 1u : 0u);
               mma_commit_pair(&c->empty[slot]);
             }
             if (stop) break;
@@ -246,18 +248,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
             const bool first = g == 0;
             if (first && pi > 0 && !pwait(pr, &c->o_free, (pi - 1) & 1, p)) { stop = true; break; }
             if (!pwait(pr, &c->p_full[go & 1], (go >> 1) & 1, p)) { stop = true; break; }
-            for (int q = 0; q < 4 && !stop; ++q) {
-              for (int jd = 0; jd < 2; ++jd, pos.advance()) {
-                const int slot = pos.slot;
-                if (!pwait(pr, &c->full[slot], pos.parity, p)) { stop = true; break; }
-                tc_fence_after();
-                const uint32_t va = v_lo + slot * (fp4::kSlot >> 4), pa = p_lo + q * (8192 >> 4);
+            for (int e = 0; e < 4; ++e, pos.advance()) {  // tile e / 2, value dims 256 (e % 2) ..
+              const int slot = pos.slot;
+              if (!pwait(pr, &c->full[slot], pos.parity, p)) { stop = true; break; }
+              tc_fence_after();
+              const uint32_t va = v_lo + slot * (fp4::kSlot >> 4), pa = p_lo + (e >> 1) * (16384 >> 4);
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                  mma_bf16_ss_pair(tmem + 128 * jd, sdesc_join(pa + kk * 2, d_hi), sdesc_join(va + kk * (2048 >> 4), d_hi),
-                                   idesc_o, (first && q == 0 && kk == 0) ? 0u : 1u);
-                mma_commit_pair(&c->empty[slot]);
-              }
+              for (int kk = 0; kk < 8; ++kk)
+                mma_bf16_ss_pair(tmem + 128 * (e & 1), sdesc_join(pa + (kk >> 2) * (8192 >> 4) + (kk & 3) * 2, d_hi),
+                                 sdesc_join(va + kk * (2048 >> 4), d_hi), idesc_o, (first && e < 2 && kk == 0) ? 0u : 1u);
+              mma_commit_pair(&c->empty[slot]);
             }
             if (stop) break;
             mma_commit_pair(&c->o_done[go & 1]);

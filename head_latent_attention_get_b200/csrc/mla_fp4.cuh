@@ -19,12 +19,13 @@
 // of MMA time for eight warps alone on an SM, against 197 for byte-permute
 // tables and 131 for the hardware conversion to f16, whose type Q lacks.
 //
-// A converter thread stages the 16 code bytes of its next eight slots in shared
-// memory of its own (cp.async, no other thread touches them): slot i of a
-// phase is converted, then its 16 bytes are refilled for slot i of the phase
-// after it, so a copy has a whole phase to arrive. Scales take registers, also
-// one phase ahead. Reading the codes again for V costs 256 bytes a token from
-// L2, a quarter of the bf16 cache's V re-read.
+// Both operands use one kind of ring entry, 128 tokens x 128 latent dims as two
+// 64-dim slices (32 KB): 64 contiguous code bytes of a token feed an entry, so
+// four lanes share a line of the cache, and the L1 tag lookups (one a clock),
+// which bounded 64-dim entries, halve. A converter thread stages the codes of
+// its next entry in shared memory of its own (cp.async), scales one phase
+// ahead in registers. Reading the codes again for V costs 256 bytes a token
+// from L2, a quarter of the bf16 cache's V re-read.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -34,19 +35,21 @@
 namespace mla {
 namespace fp4 {
 
-constexpr int kSlot = 16384;     // a K slice (128 tokens x 64 dims) or a V slot (64 tokens x 128 dims, two halves)
+constexpr int kSlot = 32768;     // ring entry: two slices of 128 tokens x 64 dims
+constexpr int kSlice = 16384;
+constexpr int kN = 3;            // ring entries
 constexpr int kGroups = 2;       // converter groups of four warps
 constexpr int kCvWarps = 4 * kGroups;
 constexpr int kRowDepth = 4;     // steps whose cache rows are resolved ahead
 constexpr int kThreads = 256 + 32 * kCvWarps;
-constexpr int kStageBytes = 8 * 4096;  // the code bytes of eight slots
+constexpr int kStageBytes = kGroups * 8192;  // the code bytes of one entry per group
 
-// Ring order of a piece of n steps: h = 0 -> K of step 0; h = 2g+1 -> K of
-// step g+1 (only if g+1 < n); h = 2g+2 -> V of step g. A K entry is nine
-// slots (eight latent slices, then RoPE), a V entry eight.
-__device__ __forceinline__ bool entry_exists(int h, int nsteps) { return !((h & 1) && (h >> 1) + 1 >= nsteps); }
-__device__ __forceinline__ bool entry_is_k(int h) { return h == 0 || (h & 1); }
-__device__ __forceinline__ int entry_step(int h) { return h == 0 ? 0 : (h & 1) ? (h >> 1) + 1 : (h >> 1) - 1; }
+// Order of a piece of n steps: phase h = 0 -> K of step 0; h = 2g+1 -> K of
+// step g+1 (only if g+1 < n); h = 2g+2 -> V of step g. A K phase is five ring
+// entries (four of latent dims, then the RoPE slice), a V phase four.
+__device__ __forceinline__ bool phase_exists(int h, int nsteps) { return !((h & 1) && (h >> 1) + 1 >= nsteps); }
+__device__ __forceinline__ bool phase_is_k(int h) { return h == 0 || (h & 1); }
+__device__ __forceinline__ int phase_step(int h) { return h == 0 ? 0 : (h & 1) ? (h >> 1) + 1 : (h >> 1) - 1; }
 
 // Steps of a piece: one 128-token tile (a single CTA) or two (a CTA pair).
 template <bool PAIR>
@@ -54,7 +57,7 @@ __device__ __forceinline__ int steps_of(const Piece& pc) {
   return PAIR ? (pc.t1 - pc.t0 + 1) >> 1 : pc.t1 - pc.t0;
 }
 
-// Walks the ring entries of every piece of a part.
+// Walks the phases of every piece of a part.
 template <bool PAIR>
 struct Phases {
   PieceIter it;
@@ -64,7 +67,7 @@ struct Phases {
   __device__ bool next() {
     if (in_piece) {
       do ++h;
-      while (h <= 2 * nsteps && !entry_exists(h, nsteps));
+      while (h <= 2 * nsteps && !phase_exists(h, nsteps));
       if (h <= 2 * nsteps) return true;
       step0 += nsteps;
     }
@@ -74,8 +77,8 @@ struct Phases {
     h = 0;
     return true;
   }
-  __device__ bool is_k() const { return entry_is_k(h); }
-  __device__ int step() const { return step0 + entry_step(h); }
+  __device__ bool is_k() const { return phase_is_k(h); }
+  __device__ int step() const { return step0 + phase_step(h); }
 };
 
 // Cache rows of the steps in flight (-1: past the request's end, outside the
@@ -87,26 +90,28 @@ struct RowTable {
   uint32_t valid[kRowDepth][8];
 };
 
-// Position in the ring: slot and the parity of its current use.
-template <int N>
+// Position in the ring: entry and the parity of its current use.
 struct RingPos {
   int slot = 0;
   uint32_t parity = 0;
   __device__ __forceinline__ void advance(int n = 1) {
     slot += n;
-    if (slot >= N) {
-      slot -= N;
+    while (slot >= kN) {
+      slot -= kN;
       parity ^= 1u;
     }
   }
+  __device__ __forceinline__ RingPos at(int n) const {
+    RingPos r = *this;
+    r.advance(n);
+    return r;
+  }
 };
 
-// 16 bytes that are read once per CTA and ring: no L1 line is kept for them.
-__device__ __forceinline__ uint4 ldg16(const uint8_t* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
+// Eight bytes that are read once: no L1 line is kept for them.
+__device__ __forceinline__ uint2 ldg8(const uint8_t* p) {
+  uint2 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
   return v;
 }
 
@@ -217,58 +222,50 @@ __device__ __forceinline__ void row_warp(const DecodeParams& p, PieceIter it, Ro
 }
 
 // ---------------------------------------------------------------- converters
-// Fills the ring. Groups of four warps take the slots of a phase in turn
-// (group g: latent slots g, g + kGroups, ..; group 0 also copies the RoPE
-// slice), so that the waits of one group hide behind the arithmetic of the
-// others. A thread converts two items of 32 codes per slot. K slot: tokens
-// 32 w + 16 j + lane % 16, half lane / 16 of the slice's 64 dims; V slot:
-// tokens 16 w + 8 j + lane % 8, quarter lane / 8 of the slot's 128 dims; eight
-// neighbouring lanes write the same chunk of eight rows, which the swizzle
-// spreads over all banks. `stage`: 16 bytes per item and thread.
-// The RoPE slice goes straight into its slot with cp.async, whose completion
-// the slot's barrier counts.
-// wait(bar, parity): the kernel's bounded wait; full(slot): the slot's barrier.
-template <bool PAIR, int NSLOTS, class Wait, class Full>
+// Fills the ring. Two groups of four warps take a phase's latent entries in
+// turn (group g: entries g and g + 2) and its RoPE slice every other step. A
+// thread converts four items of 32 codes per entry: tokens 32 w + 8 j +
+// lane % 8, quarter lane / 8 of the entry's 128 dims; eight neighbouring lanes
+// write the same chunk of eight rows, which the swizzle spreads over all banks.
+// Entry e of a phase: K, and a single CTA's V: latent dims 128 e .. of the
+// step's (own) tile; a pair's V: tile e / 2, value dims 256 (e % 2) + 128 rank ..
+// `stage`: 16 bytes per item and thread.
+// Scales: lane quarter q loads the eight scale bytes of entry q for its
+// token, and an entry's are handed round by shuffle: one request a phase.
+// The RoPE slice goes straight into its entry with cp.async, whose completion
+// the entry's barrier counts.
+// wait(bar, parity): the kernel's bounded wait; full(slot): the entry's barrier.
+template <bool PAIR, class Wait, class Full>
 __device__ __forceinline__ void convert_ring(const DecodeParams& p, const PieceIter& it, RowTable* rt, uint8_t* ring,
                                              uint4* stage, uint64_t* empty, int cw, int lane, int rank, Wait wait,
                                              Full full) {
-  constexpr int kPer = 8 / kGroups;  // latent slots of a phase per group
+  static_assert(kGroups == 2, "two entries per group and phase");
   const uint8_t* cache = static_cast<const uint8_t*>(p.kcache);
   const int grp = cw >> 2, w = cw & 3;
-  const int ktok = 32 * w + (lane & 15), khalf = lane >> 4;
-  const int vtok = 16 * w + (lane & 7), vq = lane >> 3;
+  const int tok = 32 * w + (lane & 7), q = lane >> 3;
   const int k0 = PAIR ? 128 * rank : 0;  // first token of this CTA's K tile
   stage += 32 * cw + lane;
-  // record and first dim of item (i, j) of a phase; V slot i is a pair's
-  // (64-token quarter i / 2, value dims 256 (i % 2) + 128 rank ..), a single
-  // CTA's (value dims 128 (i / 2) .., 64-token half i % 2)
-  auto row_of = [&](bool k, int step, int i, int j) {
-    const int t = k ? k0 + ktok + 16 * j : 64 * (PAIR ? i >> 1 : i & 1) + vtok + 8 * j;
-    return rt->row[step % kRowDepth][t];
+  auto record = [&](bool k, int step, int e, int j) {
+    return rt->row[step % kRowDepth][(k ? k0 : PAIR ? 128 * (e >> 1) : 0) + tok + 8 * j];
   };
-  auto dim_of = [&](bool k, int i) {
-    return k ? 64 * i + 32 * khalf : (PAIR ? 256 * (i & 1) + 128 * rank : 128 * (i >> 1)) + 32 * vq;
-  };
-  auto fetch = [&](bool k, int step, int n) {
-    const int i = grp + kGroups * n, d = dim_of(k, i);
+  auto dim_of = [&](bool k, int e) { return PAIR && !k ? 256 * (e & 1) + 128 * rank : 128 * e; };
+  auto fetch = [&](bool k, int step, int e) {
+    const int off = dim_of(k, e) / 2 + 16 * q;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int row = row_of(k, step, i, j);
-      cp_async16(stage + (2 * n + j) * (32 * kCvWarps), cache + (size_t)(row >= 0 ? row : 0) * kFp4RecordBytes + d / 2,
+    for (int j = 0; j < 4; ++j) {
+      const int row = record(k, step, e, j);
+      cp_async16(stage + j * (32 * kCvWarps), cache + (size_t)(row >= 0 ? row : 0) * kFp4RecordBytes + off,
                  row >= 0 ? 16u : 0u);
     }
+    cp_async_commit();
   };
-  auto scales = [&](bool k, int step, uint32_t (&sc)[kPer][2]) {
+  auto scales = [&](bool k, int step, uint2 (&sc)[4]) {
+    const int off = kFp4ScaleOff + dim_of(k, q) / 16;
 #pragma unroll
-    for (int n = 0; n < kPer; ++n) {
-      const int i = grp + kGroups * n, d = dim_of(k, i);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int row = row_of(k, step, i, j);
-        sc[n][j] = 0;
-        if (row >= 0)
-          sc[n][j] = *reinterpret_cast<const uint16_t*>(cache + (size_t)row * kFp4RecordBytes + kFp4ScaleOff + d / 16);
-      }
+    for (int j = 0; j < 4; ++j) {
+      const int row = record(k, step, q, j);
+      sc[j] = make_uint2(0, 0);
+      if (row >= 0) sc[j] = ldg8(cache + (size_t)row * kFp4RecordBytes + off);
     }
   };
   auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
@@ -277,19 +274,15 @@ __device__ __forceinline__ void convert_ring(const DecodeParams& p, const PieceI
     if (lane == 0) ok = wait(bar, parity);
     return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
   };
-  Phases<PAIR> nxt;         // the phase being fetched, one ahead of the phase being converted
+  Phases<PAIR> nxt;     // the phase after the one being converted
   nxt.it = it;
-  uint32_t pre[kPer][2];    // its scales
-  int seq = 0;              // ring position of the converted phase's first slot
+  uint2 pre[4];         // its scales
+  RingPos pos;          // first entry of the phase being converted
   bool have = nxt.next();
   if (have) {
     if (!wait_warp(&rt->full[0], 0)) return;
     scales(true, 0, pre);
-#pragma unroll
-    for (int n = 0; n < kPer; ++n) {
-      fetch(true, 0, n);
-      cp_async_commit();
-    }
+    fetch(true, 0, grp);
   }
   bool stop = false;
   while (have && !stop) {
@@ -301,61 +294,58 @@ __device__ __forceinline__ void convert_ring(const DecodeParams& p, const PieceI
     if (nk && !wait_warp(&rt->full[nstep % kRowDepth], (nstep / kRowDepth) & 1)) break;
     // one wait for all scales: loads share a few scoreboards, so one used
     // while younger loads are in flight would wait for those too
-    uint32_t sc[kPer][2];
+    uint2 sc[4];
 #pragma unroll
-    for (int n = 0; n < kPer; ++n)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) sc[n][j] = settle(pre[n][j]);
+    for (int j = 0; j < 4; ++j) sc[j] = make_uint2(settle(pre[j].x), settle(pre[j].y));
     if (have) scales(nk, nstep, pre);
-    // not unrolled: the unrolled loop's code left no room in the instruction
-    // cache for the other roles
+    // not unrolled: the unrolled code left no room in the instruction cache
+    // for the other roles
 #pragma unroll 1
-    for (int n = 0; n < kPer; ++n) {
-      const int sq = seq + grp + kGroups * n, slot = sq % NSLOTS;
-      cp_async_wait<kPer - 1>();  // one group per slot: the younger ones may be in flight
-      uint4 codes[2];
+    for (int e = grp; e < 4; e += 2) {
+      const RingPos at = pos.at(e);
+      cp_async_wait<0>();
+      uint4 codes[4];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) codes[j] = stage[(2 * n + j) * (32 * kCvWarps)];
-      if (!wait_warp(&empty[slot], ((sq / NSLOTS) & 1) ^ 1)) { stop = true; break; }
-      uint8_t* s = ring + slot * kSlot;
+      for (int j = 0; j < 4; ++j) codes[j] = stage[j * (32 * kCvWarps)];
+      if (e < 2) fetch(k, step, e + 2);
+      else if (have) fetch(nk, nstep, grp);
+      if (!wait_warp(&empty[at.slot], at.parity ^ 1u)) { stop = true; break; }
+      uint8_t* s = ring + at.slot * kSlot + (q >> 1) * kSlice;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        store_item(codes[j], sc[0][j], s + (k ? 0 : (vq >> 1) * 8192), k ? ktok + 16 * j : vtok + 8 * j,
-                   4 * (k ? khalf : vq & 1));
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t lo = __shfl_sync(0xffffffffu, sc[j].x, 8 * e + (lane & 7));
+        const uint32_t hi = __shfl_sync(0xffffffffu, sc[j].y, 8 * e + (lane & 7));
+        store_item(codes[j], (q & 2 ? hi : lo) >> (16 * (q & 1)), s, tok + 8 * j, 4 * (q & 1));
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(full(slot));
-      if (have) fetch(nk, nstep, n);
-      cp_async_commit();
-#pragma unroll
-      for (int m = 0; m + 1 < kPer; ++m)  // the next slot's scales move to the front
-#pragma unroll
-        for (int j = 0; j < 2; ++j) sc[m][j] = sc[m + 1][j];
+      if (lane == 0) mbar_arrive(full(at.slot));
     }
     if (stop) break;
-    seq += 8;
     if (k) {
-      if (grp == 0) {  // RoPE slice: 8 lanes per 128-byte row
-        const int slot = seq % NSLOTS;
-        if (!wait_warp(&empty[slot], ((seq / NSLOTS) & 1) ^ 1)) break;
+      if (grp == (step & 1)) {  // RoPE slice: 8 lanes per 128-byte row
+        const RingPos at = pos.at(4);
+        if (!wait_warp(&empty[at.slot], at.parity ^ 1u)) break;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int t = 32 * w + 4 * i + (lane >> 3), ch = lane & 7;
           const int row = rt->row[step % kRowDepth][k0 + t];
-          cp_async16(sw128(ring + slot * kSlot, t, ch),
+          cp_async16(sw128(ring + at.slot * kSlot, t, ch),
                      cache + (size_t)(row >= 0 ? row : 0) * kFp4RecordBytes + kFp4RopeOff + 16 * ch, row >= 0 ? 16u : 0u);
         }
-        cp_async_mbar_arrive(full(slot));
+        cp_async_mbar_arrive(full(at.slot));
         __syncwarp();
-        if (lane == 0) mbar_arrive(full(slot));
+        if (lane == 0) mbar_arrive(full(at.slot));
       }
-      ++seq;
+      pos.advance(5);
+    } else {
+      pos.advance(4);
     }
-    // the rows of a step are last read by the fetches of its V entry
-    if (have && !nk) {
+    // the rows of a step are last read by the fetches of its V phase: the one
+    // of entry grp + 2 is issued in that phase itself
+    if (!k) {
       __syncwarp();
-      if (lane == 0) mbar_arrive(&rt->empty[nstep % kRowDepth]);
+      if (lane == 0) mbar_arrive(&rt->empty[step % kRowDepth]);
     }
   }
   cp_async_wait<0>();  // no copy may land after the CTA has finished
