@@ -23,12 +23,14 @@ MLA_ERR_WORKSPACE_TOO_SMALL = 3
 MLA_ERR_CUDA = 4
 MLA_ERR_DEVICE_TIMEOUT = 5
 MLA_ERR_DEVICE_BOUNDS = 6
+MLA_ERR_DEVICE_NO_PAGES = 7
 MLA_KV_BF16 = 0
 MLA_KV_FP8_E4M3 = 1
 MLA_KV_NVFP4 = 2
 MLA_KV_FP4_E2M1 = 3
 MLA_DEVICE_STATUS_TIMEOUT = 1
 MLA_DEVICE_STATUS_BOUNDS = 2
+MLA_DEVICE_STATUS_NO_PAGES = 4
 MLA_DEBUG_WITHHOLD_SCORES = 1
 MLA_DEBUG_SKIP_COMBINE = 2
 MLA_TILE_MD_INTS = 8
@@ -100,6 +102,10 @@ def lib() -> ctypes.CDLL:
         L.mla_q_norm_rope.argtypes = [vp, vp, i, i, i, i, vp, f, vp, vp, vp]
         L.mla_out_rope_fp8.restype = i
         L.mla_out_rope_fp8.argtypes = [vp, i, i, i, i, vp, vp, vp, vp, vp]
+        L.mla_extend_tables.restype = i
+        L.mla_extend_tables.argtypes = [vp, vp, i, vp, i, vp, i, vp, i, vp, vp, vp, vp, i, vp, vp, vp]
+        L.mla_kv_append.restype = i
+        L.mla_kv_append.argtypes = [vp, ctypes.c_longlong, i, i, vp, f, vp, vp, vp, vp, vp, i, i, vp, vp, vp]
         _lib = L
     return _lib
 
@@ -233,3 +239,21 @@ def mla_q_norm_rope(q, q_out, batch, s_q, h_q, d_qk, gamma, eps, rope_cos, rope_
 def mla_out_rope_fp8(out, batch, s_q, h_q, d_qk, rope_cos, rope_sin, out_fp8, out_scale, stream=None):
     _check(lib().mla_out_rope_fp8(_ptr(out), batch, s_q, h_q, d_qk, _ptr(rope_cos), _ptr(rope_sin),
                                   _ptr(out_fp8), _ptr(out_scale), _stream(stream)), "mla_out_rope_fp8")
+
+
+def mla_extend_tables(context_lens, new_lens, batch, free_pages, free_range, num_pages, block_table,
+                      block_table_stride, seqlens, token_start, slots, positions, max_tokens, free_next, status=None,
+                      stream=None):
+    """num_free is the length of free_pages (a tensor, or None for an empty list)."""
+    num_free = 0 if free_pages is None else free_pages.numel()
+    _check(lib().mla_extend_tables(_ptr(context_lens), _ptr(new_lens), batch, _ptr(free_pages), num_free,
+                                   _ptr(free_range), num_pages, _ptr(block_table), block_table_stride, _ptr(seqlens),
+                                   _ptr(token_start), _ptr(slots), _ptr(positions), max_tokens, _ptr(free_next),
+                                   _ptr(status), _stream(stream)), "mla_extend_tables")
+
+
+def mla_kv_append(kv, kv_stride, tokens, d_qk, gamma, eps, rope_cos, rope_sin, slots, kcache, kv_scale, kv_format,
+                  num_pages, kv_out=None, status=None, stream=None):
+    _check(lib().mla_kv_append(_ptr(kv), kv_stride, tokens, d_qk, _ptr(gamma), float(eps), _ptr(rope_cos),
+                               _ptr(rope_sin), _ptr(slots), _ptr(kcache), _ptr(kv_scale), kv_format, num_pages,
+                               _ptr(kv_out), _ptr(status), _stream(stream)), "mla_kv_append")

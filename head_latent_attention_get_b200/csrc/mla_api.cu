@@ -190,6 +190,7 @@ const char* mla_status_string(mla_status_t s) {
     case MLA_ERR_CUDA: return "MLA_ERR_CUDA";
     case MLA_ERR_DEVICE_TIMEOUT: return "MLA_ERR_DEVICE_TIMEOUT";
     case MLA_ERR_DEVICE_BOUNDS: return "MLA_ERR_DEVICE_BOUNDS";
+    case MLA_ERR_DEVICE_NO_PAGES: return "MLA_ERR_DEVICE_NO_PAGES";
   }
   return "MLA_ERR_UNKNOWN";
 }
@@ -293,6 +294,7 @@ mla_status_t mla_query_device_status(const void* workspace, uint32_t* status_bit
   if (status_bits) *status_bits = bits;
   if (bits & MLA_DEVICE_STATUS_TIMEOUT) return MLA_ERR_DEVICE_TIMEOUT;
   if (bits & MLA_DEVICE_STATUS_BOUNDS) return MLA_ERR_DEVICE_BOUNDS;
+  if (bits & MLA_DEVICE_STATUS_NO_PAGES) return MLA_ERR_DEVICE_NO_PAGES;
   return MLA_OK;
 }
 

@@ -67,7 +67,8 @@ typedef enum {
   MLA_ERR_WORKSPACE_TOO_SMALL = 3, /* workspace_bytes < mla_workspace_size(...) */
   MLA_ERR_CUDA = 4,                /* a CUDA runtime/driver call failed */
   MLA_ERR_DEVICE_TIMEOUT = 5,      /* status word: a device wait hit its limit */
-  MLA_ERR_DEVICE_BOUNDS = 6        /* status word: an index/page was out of range */
+  MLA_ERR_DEVICE_BOUNDS = 6,       /* status word: an index/page was out of range */
+  MLA_ERR_DEVICE_NO_PAGES = 7      /* status word: the free-page list ran out */
 } mla_status_t;
 
 /* KV cache storage formats (mla_decode_args.kv_format). */
@@ -105,7 +106,8 @@ enum {
 /* Bits of the device status word kept at the start of the workspace. */
 enum {
   MLA_DEVICE_STATUS_TIMEOUT = 1u, /* an mbarrier wait exceeded timeout_ns */
-  MLA_DEVICE_STATUS_BOUNDS = 2u   /* page id, block-table slot or index out of range */
+  MLA_DEVICE_STATUS_BOUNDS = 2u,  /* page id, block-table slot or index out of range */
+  MLA_DEVICE_STATUS_NO_PAGES = 4u /* mla_extend_tables: too few free pages for every request */
 };
 
 /* Test and timing hooks for mla_decode_args.debug_flags (0 in normal use). */
@@ -326,6 +328,88 @@ mla_status_t mla_q_norm_rope(const void* q, void* q_out, int batch, int s_q, int
 mla_status_t mla_out_rope_fp8(const void* out, int batch, int s_q, int h_q, int d_qk, const float* rope_cos,
                               const float* rope_sin, void* out_fp8, float* out_scale, mla_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Filling the cache: the step's block tables and slots, and the new rows. Both
+ * calls are asynchronous on `stream`, allocate nothing and keep no state.
+ * `status` (device uint32, or NULL) receives MLA_DEVICE_STATUS_* bits by OR;
+ * it may be a decode workspace, whose first word is the status word, and any
+ * such word is read with mla_query_device_status and cleared with
+ * mla_clear_device_status.
+ * ------------------------------------------------------------------------- */
+
+/* Block tables and slot map of a step. Request b holds context_lens[b] tokens
+ * and gets new_lens[b] more (0 allowed):
+ *   - it takes ceil((ctx + new) / 64) - ceil(ctx / 64) pages from the free
+ *     list, in request order, and they become entries ceil(ctx / 64).. of its
+ *     block-table row (all other entries are left as they are);
+ *   - seqlens[b] = ctx + new, the cache_seqlens of the step's decode calls;
+ *   - its new tokens are [token_start[b], token_start[b] + new) of the step's
+ *     token axis (token_start: exclusive prefix sum of max(new_lens, 0), with
+ *     the total at [batch]); token i of them has positions[t] = ctx + i and
+ *     slots[t] = page * 64 + positions[t] % 64.
+ * Entries of slots and positions from the total up to max_tokens are -1.
+ * A request is refused, keeps seqlens[b] = max(ctx, 0), takes no page and has
+ * slots and positions of -1 when a length is negative, ctx + new exceeds
+ * block_table_stride * 64 or its tokens end past max_tokens
+ * (MLA_DEVICE_STATUS_BOUNDS), or when the free list does not hold its pages
+ * and those of all requests before it (MLA_DEVICE_STATUS_NO_PAGES; later
+ * requests that need no page are served). A page id outside [0, num_pages),
+ * in the free list or in the row, gives slots of -1 (and a table entry of -1)
+ * and MLA_DEVICE_STATUS_BOUNDS.
+ *   context_lens, new_lens  device int32 [batch]
+ *   free_pages   device int32 [num_free], distinct unused pages (NULL if num_free is 0)
+ *   free_range   device int32 [2]: the first unused entry of free_pages and
+ *                one past the last; a range outside [0, num_free] counts as
+ *                empty and sets MLA_DEVICE_STATUS_BOUNDS
+ *   block_table  device int32 [batch, block_table_stride], updated
+ *   seqlens      device int32 [batch]; token_start device int32 [batch + 1];
+ *   slots, positions  device int32 [max_tokens], written
+ *   free_next    device int32 [1], written: free_range[0] + pages taken, the
+ *                next step's free_range[0]
+ * The outputs must overlap neither the inputs nor each other. Errors:
+ * INVALID_ARG (null, misaligned or overlapping buffers, non-positive sizes),
+ * UNSUPPORTED (num_pages * 64 or block_table_stride * 64 above 2^31 - 1, batch
+ * or max_tokens above 2^30), CUDA. */
+mla_status_t mla_extend_tables(const int32_t* context_lens, const int32_t* new_lens, int batch,
+                               const int32_t* free_pages, int num_free, const int32_t* free_range, int num_pages,
+                               int32_t* block_table, int block_table_stride, int32_t* seqlens, int32_t* token_start,
+                               int32_t* slots, int32_t* positions, int max_tokens, int32_t* free_next,
+                               uint32_t* status, mla_stream_t stream);
+
+/* New rows into the cache. Row t of kv (bf16, kv_stride elements apart) holds
+ * d_qk values: 512 latent and 64 RoPE (576), or the 512 of an NVFP4 row.
+ *   - gamma (fp32 [512], or NULL for rows that are normalised already): the
+ *     512 latent values become x / sqrt(mean(x^2) + eps) * gamma;
+ *   - rope_cos / rope_sin (fp32 [tokens][32], both or neither): the last 64
+ *     values are rotated pair-wise by the token's angles as in mla_q_norm_rope
+ *     (512-value rows: after the norm);
+ *   - every value is rounded to bf16, and the latent values then to the
+ *     cache's format: FP8 per 128 values with scale = amax / 448 (1 if amax is
+ *     0), the code of value / scale; E2M1 per 16 values with the UE4M3 scale of
+ *     amax / 6, the code of value / scale (0 if the scale rounds to 0); all to
+ *     nearest even, saturating;
+ *   - the row goes to cache slot slots[t] (page * 64 + token of the page).
+ *     -1: the row is skipped; other values outside [0, num_pages * 64) are
+ *     skipped and set MLA_DEVICE_STATUS_BOUNDS. Two rows must not name one
+ *     slot: its record could then hold parts of both.
+ * The factor 1 / sqrt(..) is rounded to fp32 from 64-bit arithmetic and every
+ * fp32 product, sum and quotient once, so the stored bytes are a function of
+ * the inputs. NaN inputs give unspecified codes in their row.
+ *   kcache    device, format per kv_format (MLA_KV_*), 16-byte aligned;
+ *   kv_scale  MLA_KV_NVFP4: device uint8 [num_pages, 64, 32], else ignored;
+ *   kv_out    device bf16 [tokens][d_qk] or NULL: the values that the cache now
+ *             holds (what decoding reads), for attention over the new tokens;
+ *             rows without a slot are left alone. It may be kv when
+ *             kv_stride == d_qk.
+ * kv, kcache, kv_scale, kv_out and gamma 16-byte aligned, kv_stride a multiple
+ * of 8. Errors: INVALID_ARG (null or misaligned pointers, a bad format, d_qk,
+ * stride or size, one of rope_cos / rope_sin without the other, eps < 0),
+ * UNSUPPORTED (num_pages * 64 above 2^31 - 1, tokens above 2^30), CUDA. */
+mla_status_t mla_kv_append(const void* kv, long long kv_stride, int tokens, int d_qk, const float* gamma, float eps,
+                           const float* rope_cos, const float* rope_sin, const int32_t* slots, void* kcache,
+                           void* kv_scale, int kv_format, int num_pages, void* kv_out, uint32_t* status,
+                           mla_stream_t stream);
+
 /* Split-KV combine alone (mla_decode_* call it already). For every unit u
  * with n = num_splits[u+1] - num_splits[u]:
  *   n >= 2: lse = ln sum_s exp(lse_s), out = sum_s exp(lse_s - lse) * o_s
@@ -351,8 +435,8 @@ mla_status_t mla_combine_sink(const void* workspace, size_t workspace_bytes, con
                               void* out, float* lse, mla_stream_t stream);
 
 /* Reads the device status word (blocks until `stream` reaches this point).
- * Returns MLA_OK, MLA_ERR_DEVICE_TIMEOUT or MLA_ERR_DEVICE_BOUNDS (timeout
- * wins when both are set) and stores the raw bits in *status_bits when
+ * Returns MLA_OK, MLA_ERR_DEVICE_TIMEOUT, MLA_ERR_DEVICE_BOUNDS or
+ * MLA_ERR_DEVICE_NO_PAGES (the first of them that is set) and stores the raw bits in *status_bits when
  * status_bits is not NULL. The word stays set until cleared. */
 mla_status_t mla_query_device_status(const void* workspace, uint32_t* status_bits, mla_stream_t stream);
 
