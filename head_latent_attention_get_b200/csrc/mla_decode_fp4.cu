@@ -3,18 +3,17 @@
 //
 // Same computation and TMEM layout as the row-group kernel of the bf16 cache
 // (mla_decode.cu): per tile of 128 tokens
-//   S    = Q K^T     tcgen05 M=64 rows x N=128 tokens x K=576
+//   S    = Q K^T     tcgen05 M=64 rows x N=128 tokens x K=576 (f16, RoPE bf16)
 //   softmax          one thread per query row, online, O rescaled lazily
 //   O^T += V^T P^T   tcgen05 M=128 value dims (4 chunks) x N=rows x K=128
-// The keys reach the tensor core through one ring of 32 KB entries that eight
-// converter warps fill from the records (mla_fp4.cuh), in the order in which
+// The keys reach the tensor core through one ring of 32 KB entries that is
+// filled from the records (mla_fp4.cuh), in the order in which
 // the one MMA issuer consumes it: S(0), S(1), O(0), S(2), O(1), ...
 //
-// Warp roles (512 threads):
-//   0 Q via TMA, then 0 and 2 put it in the converted keys' order
-//   1 MMA issuer (+ TMEM alloc)   3 cache rows
+// Warp roles (640 threads):
+//   0 Q via TMA   1 MMA issuer (+ TMEM alloc)   2 cache rows   3 RoPE slices
 //   4-7 softmax + epilogue (row r = 16*(warp-4) + lane, lanes 0-15)
-//   8-15 converters
+//   8-11 raw copies   12-19 converters (and Q into form)
 // Every wait is bounded; on a timeout the CTA records
 // MLA_DEVICE_STATUS_TIMEOUT, stops issuing work, waits (bounded) for its own
 // copies and MMAs and exits normally.
@@ -33,28 +32,30 @@ constexpr int kTmemS = 256;            // S buffers at columns 256 and 384
 constexpr float kRescaleLog2 = 8.0f;   // rescale O only when the max grows by > 2^8
 
 struct Ctrl {
-  uint64_t q_raw, q_full, q_empty;      // q_raw: as loaded; q_full: in order (both warps)
+  uint64_t q_raw, q_full, q_empty;      // q_raw: as loaded; q_full: converter warps have it in form
   uint64_t full[kN], empty[kN];
+  uint64_t rope_free;                   // entry 1 of a K phase is consumed
   uint64_t s_full[2];
   uint64_t p_full, o_done, o_free, drain;
   uint64_t grp_sm;  // bounded barrier of the 128 softmax threads
+  float q_back[2][64];                 // [piece parity][row]: what undoes the query's scaling
   uint32_t tmem_base;
   int abort_flag;
   int rescale_flag[2];
   float alpha[64];
   float inv_l[64];
 };
-static_assert(sizeof(Ctrl) <= 1024, "control block");
+static_assert(sizeof(Ctrl) <= 1536, "control block");
 
 template <int NR>
 struct Smem {
   static constexpr int q = 0;
   static constexpr int ring = q + kQBytes;
-  static constexpr int stage = ring + kN * fp4::kSlot;
-  static constexpr int pt = stage + fp4::kStageBytes;
-  static constexpr int pt_bytes = NR * 256;  // [NR rows][128 tokens] bf16
+  static constexpr int raw = ring + kN * fp4::kSlot;
+  static constexpr int pt = (raw + fp4::kRaw * fp4::kRawBytes + 1023) / 1024 * 1024;  // swizzled
+  static constexpr int pt_bytes = NR * 256;  // [NR rows][128 tokens] f16
   static constexpr int ctrl = pt + pt_bytes;
-  static constexpr int rows = ctrl + 1024;
+  static constexpr int rows = ctrl + 1536;
   static constexpr int total = rows + (int)sizeof(fp4::RowTable);
 };
 static_assert(Smem<64>::total + 1024 <= 232448, "shared memory budget");
@@ -85,7 +86,7 @@ __global__ void __launch_bounds__(fp4::kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem + L::q;
   uint8_t* sRing = smem + L::ring;
-  uint4* sStage = reinterpret_cast<uint4*>(smem + L::stage);
+  uint8_t* sRaw = smem + L::raw;
   uint8_t* sP = smem + L::pt;
   Ctrl* c = reinterpret_cast<Ctrl*>(smem + L::ctrl);
   fp4::RowTable* rt = reinterpret_cast<fp4::RowTable*>(smem + L::rows);
@@ -96,13 +97,18 @@ __global__ void __launch_bounds__(fp4::kThreads, 1)
 
   if (threadIdx.x == 0) {
     mbar_init(&c->q_raw, 1);
-    mbar_init(&c->q_full, 2);
+    mbar_init(&c->q_full, fp4::kCvWarps);
     mbar_init(&c->q_empty, 1);
+    mbar_init(&c->rope_free, 1);
     for (int i = 0; i < kN; ++i) { mbar_init(&c->full[i], 4); mbar_init(&c->empty[i], 1); }
     for (int i = 0; i < 2; ++i) mbar_init(&c->s_full[i], 1);
     for (int i = 0; i < fp4::kRowDepth; ++i) {
       mbar_init(&rt->full[i], 1);
-      mbar_init(&rt->empty[i], fp4::kCvWarps + (SPARSE ? 4 : 0));
+      mbar_init(&rt->empty[i], fp4::kLdWarps + 1 + (SPARSE ? 4 : 0));
+    }
+    for (int i = 0; i < fp4::kRaw; ++i) {
+      mbar_init(&rt->raw_full[i], 32 * fp4::kLdWarps);
+      mbar_init(&rt->raw_empty[i], 4);
     }
     mbar_init(&c->p_full, 128);
     mbar_init(&c->o_done, 1);
@@ -129,38 +135,42 @@ __global__ void __launch_bounds__(fp4::kThreads, 1)
   it.init(p, part);
   Piece pc;
   auto wait = [&](uint64_t* bar, uint32_t parity) { return timed_wait(c, bar, parity, p); };
+  auto full = [&](int slot) { return &c->full[slot]; };
 
-  if (warp == 0 || warp == 2) {
+  if (warp == 0) {
     // ------------------------------------------------------------ Q
-    int pi = 0, q_issued = 0;
-    while (it.next(pc)) {
-      if (warp == 0 && lane == 0 && timed_wait(c, &c->q_empty, (pi & 1) ^ 1, p)) {
+    if (lane == 0) {
+      int pi = 0, q_issued = 0;
+      while (it.next(pc)) {
+        if (!timed_wait(c, &c->q_empty, (pi & 1) ^ 1, p)) break;
         mbar_arrive_expect_tx(&c->q_raw, kQBytes);
         for (int j = 0; j < 9; ++j) tma_load_2d(sQ + j * 8192, &tm_q, &c->q_raw, 64 * j, pc.unit * p.rows);
         ++q_issued;
+        ++pi;
       }
-      __syncwarp();
-      bool ok = true;
-      if (lane == 0) ok = timed_wait(c, &c->q_raw, pi & 1, p);
-      if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) break;
-      fp4::order_query_tile(sQ, lane + 16 * warp, 64);
+      if (q_issued > 0) mbar_wait(&c->q_raw, (uint32_t)((q_issued - 1) & 1), p.timeout_ns);
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    fp4::row_warp<false, SPARSE>(p, it, rt, lane, 0, wait);
+  } else if (warp == 3) {
+    fp4::load_rope<false>(p, it, rt, sRing, &c->rope_free, lane, 0, wait, full);
+  } else if (warp >= 8 && warp < 12) {
+    fp4::load_raw<false>(p, it, rt, sRaw, warp - 8, lane, 0, wait);
+  } else if (warp >= 12) {
+    fp4::convert_ring<false>(it, rt, sRing, sRaw, c->empty, warp - 12, lane, wait, full, [&](int piece) {
+      if (!fp4::wait_warp(&c->q_raw, piece & 1, lane, wait)) return false;
+      fp4::scale_query_rows(sQ, c->q_back[piece & 1], rows_here, warp - 12, lane);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&c->q_full);
-      ++pi;
-    }
-    if (warp == 0 && lane == 0 && q_issued > 0) mbar_wait(&c->q_raw, (uint32_t)((q_issued - 1) & 1), p.timeout_ns);
-    __syncwarp();
-  } else if (warp == 3) {
-    fp4::row_warp<false, SPARSE>(p, it, rt, lane, wait);
-  } else if (warp >= 8) {
-    fp4::convert_ring<false>(p, it, rt, sRing, sStage, c->empty, warp - 8, lane, 0, wait,
-                             [&](int slot) { return &c->full[slot]; });
+      return true;
+    });
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer: S(0), S(1), O(0), S(2), O(1), ...
     if (elect_one()) {
-      const uint32_t idesc_s = idesc_bf16(64, 128, false, false);
-      const uint32_t idesc_o = idesc_bf16(128, NR, true, false);
+      const uint32_t idesc_s = idesc_f16(64, 128, false, false), idesc_r = idesc_bf16(64, 128, false, false);
+      const uint32_t idesc_o = idesc_f16(128, NR, true, false);
       // descriptors: Q, K and P^T are K-major, V is MN-major (slices 16 KB apart)
       const uint32_t q_lo = sdesc_lo(smem_u32(sQ), 16), k_lo = sdesc_lo(smem_u32(sRing), 16);
       const uint32_t v_lo = sdesc_lo(smem_u32(sRing), fp4::kSlice), p_lo = sdesc_lo(smem_u32(sP), 16);
@@ -187,9 +197,10 @@ __global__ void __launch_bounds__(fp4::kThreads, 1)
               for (int kk = 0; kk < 8; ++kk)
                 if (kk < 4 || e < 4)
                   mma_bf16_ss(d, sdesc_join(qa + (kk >> 2) * (8192 >> 4) + (kk & 3) * 2, d_hi),
-                              sdesc_join(kb + (kk >> 2) * (fp4::kSlice >> 4) + (kk & 3) * 2, d_hi), idesc_s,
+                              sdesc_join(kb + (kk >> 2) * (fp4::kSlice >> 4) + (kk & 3) * 2, d_hi), e < 4 ? idesc_s : idesc_r,
                               (e | kk) != 0 ? 1u : 0u);
               mma_commit(&c->empty[slot]);
+              if (e == 1) mma_commit(&c->rope_free);
             }
             if (stop) break;
             if (!(gs == 0 && (p.debug_flags & MLA_DEBUG_WITHHOLD_SCORES))) mma_commit(&c->s_full[gs & 1]);
@@ -229,9 +240,8 @@ __global__ void __launch_bounds__(fp4::kThreads, 1)
     const bool owner = lane < 16;
     const bool rvalid = owner && r < rows_here;
     const uint32_t lane_base = (uint32_t)(32 * q4) << 16;
-    const float thresh = kRescaleLog2 / p.scale_log2;    // raw-score units
     uint32_t gph = 0;
-    int gt = 0;
+    int gt = 0, pi = 0;
     bool stop = false;
     while (!stop && it.next(pc)) {
       const int req = unit_req(p, pc.unit);
@@ -242,7 +252,7 @@ __global__ void __launch_bounds__(fp4::kThreads, 1)
         limit = Ls;
         if (p.causal) limit = Ls - p.s_q + row_query(p, pc.unit, grow) + 1;
       }
-      float m_used = -INFINITY, l_sum = 0.f;
+      float m_used = -INFINITY, l_sum = 0.f, scale_log2 = 0.f;  // scale_log2: of this row's raw scores
       int last_gt = -1;
       for (int k = pc.t0; k < pc.t1 && !stop; ++k, ++gt) {
         const int b = gt & 1;
@@ -265,6 +275,7 @@ __global__ void __launch_bounds__(fp4::kThreads, 1)
         if (!rvalid) vmask = make_uint4(0, 0, 0, 0);
         if (!timed_wait(c, &c->s_full[b], (gt >> 1) & 1, p)) { stop = true; break; }
         tc_fence_after();
+        if (k == pc.t0) scale_log2 = p.scale_log2 * c->q_back[pi & 1][r & 63];
         const uint32_t s_addr = tmem + lane_base + kTmemS + 128 * b;
         // pass 1: tile max
         float tmax = -INFINITY;
@@ -279,16 +290,16 @@ __global__ void __launch_bounds__(fp4::kThreads, 1)
         }
         float alpha = 1.f;
         int need = 0;
-        if (tmax > m_used + thresh || (m_used == -INFINITY && tmax > -INFINITY)) {
+        if ((tmax - m_used) * scale_log2 > kRescaleLog2) {  // also for the first keys; never for -inf - -inf
           const float m_new = tmax;
-          alpha = (m_used == -INFINITY) ? 0.f : ex2_approx((m_used - m_new) * p.scale_log2);
+          alpha = (m_used == -INFINITY) ? 0.f : ex2_approx((m_used - m_new) * scale_log2);
           need = (k != pc.t0) && (m_used != -INFINITY);
           m_used = m_new;
           l_sum *= alpha;
         }
-        // pass 2: probabilities (a masked score is -inf: e^-inf = 0) -> bf16, staged
+        // pass 2: probabilities (a masked score is -inf: e^-inf = 0) -> f16, staged
         // in TMEM over the S columns already read (tokens 32w.. -> columns 16w..)
-        const float mc = (m_used == -INFINITY ? 0.f : m_used) * p.scale_log2;
+        const float mc = (m_used == -INFINITY ? 0.f : m_used) * scale_log2;
         float part = 0.f;
 #pragma unroll 1
         for (int w = 0; w < 4; ++w) {
@@ -299,9 +310,9 @@ __global__ void __launch_bounds__(fp4::kThreads, 1)
           uint32_t pk[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const float p0 = ex2_approx(fmaf(__uint_as_float(sv[2 * i]), p.scale_log2, -mc));
-            const float p1 = ex2_approx(fmaf(__uint_as_float(sv[2 * i + 1]), p.scale_log2, -mc));
-            pk[i] = pack_bf16x2(p0, p1);
+            const float p0 = ex2_approx(fmaf(__uint_as_float(sv[2 * i]), scale_log2, -mc));
+            const float p1 = ex2_approx(fmaf(__uint_as_float(sv[2 * i + 1]), scale_log2, -mc));
+            pk[i] = pack_f16x2(p0, p1);
             part += p0 + p1;
           }
           tmem_st16(s_addr + 16 * w, pk);
@@ -362,8 +373,8 @@ __global__ void __launch_bounds__(fp4::kThreads, 1)
       if (owner) {
         float inv = 0.f, lse = -INFINITY;
         if (l_sum > 0.f) {
-          inv = fp4::kOutScale / l_sum;
-          lse = m_used * p.scale + logf(l_sum);
+          inv = 1.f / l_sum;
+          lse = m_used * scale_log2 * 0.693147181f + logf(l_sum);
         }
         if (pc.single && rvalid && p.sink != nullptr) inv *= fold_sink(lse, p.sink[row_head(p, pc.unit, row0 + r)]);
         c->inv_l[r] = inv;
@@ -376,7 +387,7 @@ __global__ void __launch_bounds__(fp4::kThreads, 1)
       if (!group_sync(c, &c->grp_sm, gph, p)) { stop = true; break; }
 #pragma unroll 1
       for (int m = 0; m < 4; ++m) {
-        const int d = 128 * m + 32 * q4 + (lane & 24) + fp4::element_of(lane & 7);
+        const int d = 128 * m + 32 * q4 + lane;
 #pragma unroll 1
         for (int c16 = 0; c16 < NR / 16; ++c16) {
           uint32_t ov[16];
@@ -399,6 +410,7 @@ __global__ void __launch_bounds__(fp4::kThreads, 1)
       tc_fence_before();
       if (!group_sync(c, &c->grp_sm, gph, p)) { stop = true; break; }
       mbar_arrive(&c->o_free);
+      ++pi;
     }
   }
 

@@ -7,16 +7,16 @@
 // tile r and, for all 256 tokens, V of its value dims {256j + 128r + [0,128)}:
 //   S = Q K^T   pair MMA M=128 (64 rows per CTA) x N=256 tokens x K=576
 //   O = P V     pair MMA M=128 x N=256 value dims x K=256 tokens, twice
-// Each CTA's eight converter warps fill its ring from the records
+// Each CTA's ring is filled from the records
 // (mla_fp4.cuh) in the order in which the even CTA's MMA issuer consumes it.
 //
-// Warp roles (512 threads per CTA):
-//   0 Q via TMA, then 0 and 3 put it in the converted keys' order (both CTAs)
+// Warp roles (640 threads per CTA):
+//   0 Q via TMA (both CTAs)
 //   1 TMEM allocation (both); MMA issue (even CTA); forwarding of the odd
 //     CTA's slot completions (odd CTA)
-//   2 cache rows
+//   2 cache rows   3 RoPE slices
 //   4-7 softmax + epilogue (both): thread i = (row i % 64, token half i / 64)
-//   8-15 converters
+//   8-11 raw copies   12-19 converters (and Q into form)
 // All waits are bounded; a timeout sets MLA_DEVICE_STATUS_TIMEOUT, raises the
 // abort flag of both CTAs, and every role winds down to the final cluster
 // barrier, which both CTAs always reach.
@@ -37,30 +37,31 @@ constexpr float kRescaleLog2 = 8.0f;
 
 struct Ctrl {
   // barriers counted on the even CTA (the MMA issuer) ...
-  uint64_t q_full;                     // 4 arrivals: both CTAs' Q is in order
+  uint64_t q_full;                     // 16 arrivals: both CTAs' converter warps have Q in form
   uint64_t full[kN];                   // 8 converter warps + 1 forward from the odd CTA
   uint64_t p_full[2], o_free;          // 8 arrivals: 4 softmax warps x 2 CTAs
   uint64_t drain;
   // ... and in each CTA
   uint64_t q_raw;                      // Q as loaded
-  uint64_t q_empty, empty[kN];         // pair-MMA commits
+  uint64_t q_empty, empty[kN], rope_free;  // pair-MMA commits; rope_free: entry 1 of a K phase
   uint64_t s_full[2], o_done[2];       // pair-MMA commits; o_done[g & 1] completes O of step g
   uint64_t v_loc[kN];                  // odd CTA: its 8 converter warps
   uint64_t grp_sm;                     // 128 softmax threads
+  float q_back[2][64];                 // [piece parity][row]: what undoes the query's scaling
   uint32_t tmem_base;
   int abort_flag;
   float mx[2][2][64];                  // [step parity][token half][row]: per-half tile max
   float lx[2][64];                     // [token half][row]: per-half row sum
 };
-static_assert(sizeof(Ctrl) <= 2048, "control block");
+static_assert(sizeof(Ctrl) <= 2560, "control block");
 
 struct Smem {
   static constexpr int q = 0;
   static constexpr int ring = q + kQBytes;
-  static constexpr int stage = ring + kN * fp4::kSlot;
-  static constexpr int pt = stage + fp4::kStageBytes;
+  static constexpr int raw = ring + kN * fp4::kSlot;
+  static constexpr int pt = (raw + fp4::kRaw * fp4::kRawBytes + 1023) / 1024 * 1024;  // swizzled
   static constexpr int ctrl = pt + kPBytes;
-  static constexpr int rows = ctrl + 2048;
+  static constexpr int rows = ctrl + 2560;
   static constexpr int total = rows + (int)sizeof(fp4::RowTable);
 };
 static_assert(Smem::total + 1024 <= 232448, "shared memory budget");
@@ -110,7 +111,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem + Smem::q;
   uint8_t* sRing = smem + Smem::ring;
-  uint4* sStage = reinterpret_cast<uint4*>(smem + Smem::stage);
+  uint8_t* sRaw = smem + Smem::raw;
   uint8_t* sP = smem + Smem::pt;
   Ctrl* c = reinterpret_cast<Ctrl*>(smem + Smem::ctrl);
   fp4::RowTable* rt = reinterpret_cast<fp4::RowTable*>(smem + Smem::rows);
@@ -125,20 +126,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
   const int row0 = 64 * (int)pr.rank;   // first row of this CTA within a unit
 
   if (threadIdx.x == 0) {
-    mbar_init(&c->q_full, 4);
+    mbar_init(&c->q_full, 2 * fp4::kCvWarps);
     mbar_init(&c->q_raw, 1);
     for (int i = 0; i < kN; ++i) mbar_init(&c->full[i], 4 + 1);
     for (int i = 0; i < 2; ++i) mbar_init(&c->p_full[i], 8);
     mbar_init(&c->o_free, 8);
     mbar_init(&c->drain, 1);
     mbar_init(&c->q_empty, 1);
+    mbar_init(&c->rope_free, 1);
     for (int i = 0; i < kN; ++i) mbar_init(&c->empty[i], 1);
     for (int i = 0; i < 2; ++i) mbar_init(&c->s_full[i], 1);
     for (int i = 0; i < 2; ++i) mbar_init(&c->o_done[i], 1);
     for (int i = 0; i < kN; ++i) mbar_init(&c->v_loc[i], 4);
     for (int i = 0; i < fp4::kRowDepth; ++i) {
       mbar_init(&rt->full[i], 1);
-      mbar_init(&rt->empty[i], fp4::kCvWarps + (SPARSE ? 4 : 0));
+      mbar_init(&rt->empty[i], fp4::kLdWarps + 1 + (SPARSE ? 4 : 0));
+    }
+    for (int i = 0; i < fp4::kRaw; ++i) {
+      mbar_init(&rt->raw_full[i], 32 * fp4::kLdWarps);
+      mbar_init(&rt->raw_empty[i], 4);
     }
     mbar_init(&c->grp_sm, 128);
     c->abort_flag = 0;
@@ -159,33 +165,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
   it.init(p, part);
   Piece pc;
   auto wait = [&](uint64_t* bar, uint32_t parity) { return pwait(pr, bar, parity, p); };
+  auto full = [&](int slot) { return pr.leader ? &c->full[slot] : &c->v_loc[slot]; };
 
-  if (warp == 0 || warp == 3) {
+  if (warp == 0) {
     // ------------------------------------------------------------ Q
-    int pi = 0, q_issued = 0;
-    while (it.next(pc)) {
-      if (warp == 0 && lane == 0 && pwait(pr, &c->q_empty, (pi & 1) ^ 1, p)) {
+    if (lane == 0) {
+      int pi = 0, q_issued = 0;
+      while (it.next(pc)) {
+        if (!pwait(pr, &c->q_empty, (pi & 1) ^ 1, p)) break;
         mbar_arrive_expect_tx(&c->q_raw, kQBytes);
         for (int j = 0; j < 9; ++j) tma_load_2d(sQ + j * 8192, &tm_q, &c->q_raw, 64 * j, pc.unit * p.rows + row0);
         ++q_issued;
+        ++pi;
       }
-      __syncwarp();
-      bool ok = true;
-      if (lane == 0) ok = pwait(pr, &c->q_raw, pi & 1, p);
-      if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) break;
-      fp4::order_query_tile(sQ, lane + (warp == 0 ? 0 : 32), 64);
+      if (q_issued > 0) mbar_wait(&c->q_raw, (uint32_t)((q_issued - 1) & 1), p.timeout_ns);
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    fp4::row_warp<true, SPARSE>(p, it, rt, lane, (int)pr.rank, wait);
+  } else if (warp == 3) {
+    fp4::load_rope<true>(p, it, rt, sRing, &c->rope_free, lane, (int)pr.rank, wait, full);
+  } else if (warp >= 8 && warp < 12) {
+    fp4::load_raw<true>(p, it, rt, sRaw, warp - 8, lane, (int)pr.rank, wait);
+  } else if (warp >= 12) {
+    fp4::convert_ring<true>(it, rt, sRing, sRaw, c->empty, warp - 12, lane, wait, full, [&](int piece) {
+      if (!fp4::wait_warp(&c->q_raw, piece & 1, lane, wait)) return false;
+      fp4::scale_query_rows(sQ, c->q_back[piece & 1], min(64, p.rows - row0), warp - 12, lane);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) arrive_leader(pr, &c->q_full);
-      ++pi;
-    }
-    if (warp == 0 && lane == 0 && q_issued > 0) mbar_wait(&c->q_raw, (uint32_t)((q_issued - 1) & 1), p.timeout_ns);
-    __syncwarp();
-  } else if (warp == 2) {
-    fp4::row_warp<true, SPARSE>(p, it, rt, lane, wait);
-  } else if (warp >= 8) {
-    fp4::convert_ring<true>(p, it, rt, sRing, sStage, c->empty, warp - 8, lane, (int)pr.rank, wait,
-                            [&](int slot) { return pr.leader ? &c->full[slot] : &c->v_loc[slot]; });
+      return true;
+    });
   } else if (warp == 1 && !pr.leader) {
     // ------------------------------------------------------------ odd CTA: forward slot completions
     if (lane == 0) {
@@ -205,8 +215,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer: S(0), S(1), O(0), S(2), O(1), ...
-    const uint32_t idesc_s = idesc_bf16(128, 256, false, false);
-    const uint32_t idesc_o = idesc_bf16(128, 256, false, true);
+    const uint32_t idesc_s = idesc_f16(128, 256, false, false), idesc_r = idesc_bf16(128, 256, false, false);
+    const uint32_t idesc_o = idesc_f16(128, 256, false, true);
     // descriptors: Q, K and P are K-major, V is MN-major (slices 16 KB apart)
     const uint32_t q_lo = sdesc_lo(smem_u32(sQ), 16), k_lo = sdesc_lo(smem_u32(sRing), 16);
     const uint32_t v_lo = sdesc_lo(smem_u32(sRing), fp4::kSlice), p_lo = sdesc_lo(smem_u32(sP), 16);
@@ -236,9 +246,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
               for (int kk = 0; kk < 8; ++kk)
                 if (kk < 4 || e < 4)
                   mma_bf16_ss_pair(d, sdesc_join(qa + (kk >> 2) * (8192 >> 4) + (kk & 3) * 2, d_hi),
-                                   sdesc_join(kb + (kk >> 2) * (fp4::kSlice >> 4) + (kk & 3) * 2, d_hi), idesc_s,
+                                   sdesc_join(kb + (kk >> 2) * (fp4::kSlice >> 4) + (kk & 3) * 2, d_hi), e < 4 ? idesc_s : idesc_r,
                                    (e | kk) != 0 ? 1u : 0u);
               mma_commit_pair(&c->empty[slot]);
+              if (e == 1) mma_commit_pair(&c->rope_free);
             }
             if (stop) break;
             if (!(gs == 0 && (p.debug_flags & MLA_DEBUG_WITHHOLD_SCORES))) mma_commit_pair(&c->s_full[b]);
@@ -277,15 +288,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
     const int grow = row0 + row;                          // row within the unit
     const bool rvalid = grow < p.rows;
     const uint32_t lane_base = (uint32_t)(32 * (warp - 4)) << 16;
-    const float thresh = kRescaleLog2 / p.scale_log2;     // raw-score units
     uint32_t gph = 0;
-    int gt = 0;
+    int gt = 0, pi = 0;
     bool stop = false;
     while (!stop && it.next(pc)) {
       const int req = unit_req(p, pc.unit);
       const int Ls = p.seqlens[req];
       const int limit = p.causal ? Ls - p.s_q + row_query(p, pc.unit, grow) + 1 : Ls;
-      float m_used = -INFINITY, l_sum = 0.f;
+      float m_used = -INFINITY, l_sum = 0.f, scale_log2 = 0.f;  // scale_log2: of this row's raw scores
       int last_gt = -1;
       for (int k = pc.t0; k < pc.t1 && !stop; k += 2, ++gt) {
         const int b = gt & 1;
@@ -308,6 +318,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
         }
         if (!pwait(pr, &c->s_full[b], (gt >> 1) & 1, p)) { stop = true; break; }
         tc_fence_after();
+        if (k == pc.t0) scale_log2 = p.scale_log2 * c->q_back[pi & 1][row];
         const uint32_t s_addr = tmem + lane_base + kTmemS + 128 * b;
         // pass 1: max over this thread's 128 keys
         float tmax = -INFINITY;
@@ -326,13 +337,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
         // both threads of a row take the same decision from the same values
         float alpha = 1.f;
         bool need = false;
-        if (tmax > m_used + thresh || (m_used == -INFINITY && tmax > -INFINITY)) {
-          alpha = (m_used == -INFINITY) ? 0.f : ex2_approx((m_used - tmax) * p.scale_log2);
+        if ((tmax - m_used) * scale_log2 > kRescaleLog2) {  // also for the first keys; never for -inf - -inf
+          alpha = (m_used == -INFINITY) ? 0.f : ex2_approx((m_used - tmax) * scale_log2);
           need = (k != pc.t0) && (m_used != -INFINITY);
           m_used = tmax;
           l_sum *= alpha;
         }
-        // pass 2: probabilities (a masked score is -inf: e^-inf = 0) -> bf16 -> the P buffer,
+        // pass 2: probabilities (a masked score is -inf: e^-inf = 0) -> f16 -> the P buffer,
         // K-major [64 rows][64 keys] per slice: keys 64s.. in slice s; this
         // thread's keys are 128*half + [0,128), slices 2*half and 2*half + 1.
         // The single P buffer was last read by the O product of step gt - 1,
@@ -340,7 +351,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
         // the next completion of the same barrier, needs this thread's P, so
         // the parity wait never falls two phases behind.) The first
         // quarter is computed into registers while that product runs.
-        const float mc = (m_used == -INFINITY ? 0.f : m_used) * p.scale_log2;
+        const float mc = (m_used == -INFINITY ? 0.f : m_used) * scale_log2;
         float part = 0.f;
         auto probs = [&](int w, uint32_t (&pk)[16]) {
           uint32_t sv[32];
@@ -349,9 +360,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
           fp4::mask_scores(sv, pick4u(vm, w));
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const float p0 = ex2_approx(fmaf(__uint_as_float(sv[2 * i]), p.scale_log2, -mc));
-            const float p1 = ex2_approx(fmaf(__uint_as_float(sv[2 * i + 1]), p.scale_log2, -mc));
-            pk[i] = pack_bf16x2(p0, p1);
+            const float p0 = ex2_approx(fmaf(__uint_as_float(sv[2 * i]), scale_log2, -mc));
+            const float p1 = ex2_approx(fmaf(__uint_as_float(sv[2 * i + 1]), scale_log2, -mc));
+            pk[i] = pack_f16x2(p0, p1);
             part += p0 + p1;
           }
         };
@@ -404,8 +415,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
       tc_fence_after();
       float inv = 0.f, lse = -INFINITY;
       if (l_tot > 0.f) {
-        inv = fp4::kOutScale / l_tot;
-        lse = m_used * p.scale + logf(l_tot);
+        inv = 1.f / l_tot;
+        lse = m_used * scale_log2 * 0.693147181f + logf(l_tot);
       }
       if (pc.single && rvalid && p.sink != nullptr) inv *= fold_sink(lse, p.sink[row_head(p, pc.unit, grow)]);
       const size_t orow = (size_t)pc.unit * p.rows + grow;
@@ -413,8 +424,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
         if (pc.single) p.lse[orow] = lse;
         else p.ws_lse[(size_t)pc.ws_idx * p.rows + grow] = lse;
       }
-      // column of value dim i among 16 columns (the converted order of each group of 8)
-      auto position = [](int i) { return (i & 8) | ((i & 3) << 1) | ((i >> 2) & 1); };
 #pragma unroll 1
       for (int jd = 0; jd < 2; ++jd) {
         const int d0 = 256 * jd + 128 * half;
@@ -428,7 +437,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
               uint32_t pk[8];
 #pragma unroll
               for (int i = 0; i < 8; ++i)
-                pk[i] = pack_bf16x2(__uint_as_float(ov[position(2 * i)]) * inv, __uint_as_float(ov[position(2 * i + 1)]) * inv);
+                pk[i] = pack_bf16x2(__uint_as_float(ov[2 * i]) * inv, __uint_as_float(ov[2 * i + 1]) * inv);
               uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + orow * kDv + d0 + 16 * c16);
               dst[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
               dst[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
@@ -436,9 +445,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
               float4* dst = reinterpret_cast<float4*>(p.ws_o + ((size_t)pc.ws_idx * p.rows + grow) * kDv + d0 + 16 * c16);
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                dst[i] = make_float4(__uint_as_float(ov[position(4 * i)]) * inv, __uint_as_float(ov[position(4 * i + 1)]) * inv,
-                                     __uint_as_float(ov[position(4 * i + 2)]) * inv,
-                                     __uint_as_float(ov[position(4 * i + 3)]) * inv);
+                dst[i] = make_float4(__uint_as_float(ov[4 * i]) * inv, __uint_as_float(ov[4 * i + 1]) * inv,
+                                     __uint_as_float(ov[4 * i + 2]) * inv,
+                                     __uint_as_float(ov[4 * i + 3]) * inv);
             }
           }
         }
@@ -446,6 +455,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) arrive_leader(pr, &c->o_free);
+      ++pi;
     }
   }
 

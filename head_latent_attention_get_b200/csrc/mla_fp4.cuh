@@ -4,28 +4,27 @@
 // token records into tensor-core operands.
 //
 // A record is 256 bytes of E2M1 pairs, 32 UE4M3 scales (one per 16 latent
-// values) and 64 bf16 RoPE dims. Latent values become bf16 without rounding:
-// an E2M1 x UE4M3 product has at most 6 significant bits.
-//
-// Conversion: a nibble's three magnitude bits, put where a bf16 has the two
-// low exponent bits and the top mantissa bit, read as its value times 2^-126
-// (exponent field 0 is the subnormal 0.5); one multiplication by scale * 2^119
-// gives value * 2^-7 and the sign bit is moved along, five instructions for
-// two values. The 2^7 is put back in the query (K) and the output (V). Both
-// halves of a 32-bit word are worked on at once, so the eight values of a word
-// come out as elements 0 4 1 5 2 6 3 7: the query is put in the same order
-// before its first use, and the output is written back in order.
-// The five instructions bound the kernels: 142 clk of a 16 KB slot's ~256 clk
-// of MMA time for eight warps alone on an SM, against 197 for byte-permute
-// tables and 131 for the hardware conversion to f16, whose type Q lacks.
+// values) and 64 bf16 RoPE dims. Latent values become f16, without rounding: an
+// E2M1 x UE4M3 product has at most 6 significant bits and lies in [2^-10, 2688].
+// The hardware turns a byte of codes into two f16, which one multiplication
+// scales: 11 instructions for eight values, against 17 (integer shifts and
+// masks) or 19 (byte-permute tables) for bf16. One MMA wants one type for both
+// operands, so the query's latent part is f16 too, each row times a power of
+// two that puts its largest value at 2^11..2^12: what an f16 then cannot hold
+// is below 2^-36 of it, far under the fp32 accumulation. The RoPE part stays
+// bf16 on both sides (times the same power), in MMAs of its own into the same
+// accumulator. Probabilities are f16.
 //
 // Both operands use one kind of ring entry, 128 tokens x 128 latent dims as two
 // 64-dim slices (32 KB): 64 contiguous code bytes of a token feed an entry, so
-// four lanes share a line of the cache, and the L1 tag lookups (one a clock),
-// which bounded 64-dim entries, halve. A converter thread stages the codes of
-// its next entry in shared memory of its own (cp.async), scales one phase
-// ahead in registers. Reading the codes again for V costs 256 bytes a token
-// from L2, a quarter of the bf16 cache's V re-read.
+// four lanes share a line of the cache, and the L1 tag lookups (one a clock)
+// are half of those of 64-dim entries. Reading the codes again for V costs 256
+// bytes a token from L2, a quarter of the bf16 cache's V re-read.
+//
+// The work is cut by latency: one warp resolves rows, four copy raw bytes, one
+// the RoPE slices, eight only convert (two groups on alternate entries), so no
+// role waits for another's round trips. With the copies in the converter
+// warps an entry took 1.7x as long.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -41,8 +40,10 @@ constexpr int kN = 3;            // ring entries
 constexpr int kGroups = 2;       // converter groups of four warps
 constexpr int kCvWarps = 4 * kGroups;
 constexpr int kRowDepth = 4;     // steps whose cache rows are resolved ahead
-constexpr int kThreads = 256 + 32 * kCvWarps;
-constexpr int kStageBytes = kGroups * 8192;  // the code bytes of one entry per group
+constexpr int kLdWarps = 4;
+constexpr int kThreads = 256 + 32 * (kLdWarps + kCvWarps);
+constexpr int kRaw = 2;                    // raw buffers: 8 KB of codes, 1 KB of scales
+constexpr int kRawBytes = 8192 + 1024;
 
 // Order of a piece of n steps: phase h = 0 -> K of step 0; h = 2g+1 -> K of
 // step g+1 (only if g+1 < n); h = 2g+2 -> V of step g. A K phase is five ring
@@ -85,7 +86,8 @@ struct Phases {
 // piece or an ignored index: converted to zeros), and with token-sparse
 // indices the key validity bits (word w, bit i = key 32w + i of the step).
 struct RowTable {
-  uint64_t full[kRowDepth], empty[kRowDepth];
+  uint64_t full[kRowDepth], empty[kRowDepth];  // empty: loader warps, the RoPE warp (and, sparse, the softmax warps)
+  uint64_t raw_full[kRaw], raw_empty[kRaw];    // 128 loader threads; 4 converter warps
   int32_t row[kRowDepth][256];
   uint32_t valid[kRowDepth][8];
 };
@@ -108,67 +110,67 @@ struct RingPos {
   }
 };
 
-// Eight bytes that are read once: no L1 line is kept for them.
-__device__ __forceinline__ uint2 ldg8(const uint8_t* p) {
-  uint2 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
-  return v;
-}
-
 // ---------------------------------------------------------------- conversions
-// Eight E2M1 codes (one word, element i in nibble i) times a scale -> 8 bf16 in
-// element order 0 4 1 5 2 6 3 7. s: the scale * 2^119, twice.
-__device__ __forceinline__ uint4 e2m1x8(uint32_t w, __nv_bfloat162 s) {
-  constexpr uint32_t kSign = 0x80008000u, kMag = 0x01C001C0u;
-  uint32_t o[4] = {((w << 12) & kSign) | ((w << 6) & kMag), ((w << 8) & kSign) | ((w << 2) & kMag),
-                   ((w << 4) & kSign) | ((w >> 2) & kMag), (w & kSign) | ((w >> 6) & kMag)};
+// Eight E2M1 codes (one word, element i in nibble i) times a scale -> 8 f16.
+__device__ __forceinline__ uint4 e2m1x8(uint32_t w, __half2 s) {
+  uint32_t o[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 v = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&o[i]), s);
+    const __half2_raw hr = __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)((w >> (8 * i)) & 0xFFu), __NV_E2M1);
+    const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&hr), s);
     o[i] = *reinterpret_cast<const uint32_t*>(&v);
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
-// Position within an 8-element group -> element.
-__device__ __forceinline__ int element_of(int pos) { return (pos >> 1) | ((pos & 1) << 2); }
-// A 16-byte chunk of the query: times 2^7, in the converted keys' order.
-__device__ __forceinline__ uint4 order_query(uint4 v) {
-  const __nv_bfloat162 f = __float2bfloat162_rn(128.f);
-  uint32_t o[4] = {__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
-                   __byte_perm(v.y, v.w, 0x7632)};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 t = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&o[i]), f);
-    o[i] = *reinterpret_cast<const uint32_t*>(&t);
-  }
-  return make_uint4(o[0], o[1], o[2], o[3]);
-}
-constexpr float kOutScale = 128.f;  // what the converted V lacks
-
-// Puts the latent slices of a query tile (64 rows) in order: thread t of `n`.
-__device__ __forceinline__ void order_query_tile(uint8_t* q, int t, int n) {
-#pragma unroll 4
-  for (int i = t; i < 8 * 512; i += n) {  // chunk order within a slice does not matter
-    uint4* c = reinterpret_cast<uint4*>(q) + i;
-    *c = order_query(*c);
-  }
-}
-
 // 32 codes and their two UE4M3 scale bytes (bit 7 ignored) -> chunks c0..c0+3
 // of 128-byte row `row` of a swizzled tile.
 __device__ __forceinline__ void store_item(uint4 codes, uint32_t scales, uint8_t* tile, int row, int c0) {
   const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(scales & 0x7F7Fu), __NV_E4M3);
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hr));
-  const __nv_bfloat162 s0 = __float2bfloat162_rn(f.x * 0x1p119f), s1 = __float2bfloat162_rn(f.y * 0x1p119f);
+  const __half2 sc = *reinterpret_cast<const __half2*>(&hr);
+  const __half2 s0 = __low2half2(sc), s1 = __high2half2(sc);
   const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(sw128(tile, row, c0 + i)) = e2m1x8(w[i], i < 2 ? s0 : s1);
 }
-// Copies a loaded word with an instruction that the compiler keeps where it is.
-__device__ __forceinline__ uint32_t settle(uint32_t a) {
-  uint32_t b;
-  asm volatile("mov.b32 %0, %1;" : "=r"(b) : "r"(a));
-  return b;
+
+// ---------------------------------------------------------------- query
+// Puts a query tile (nine 64-row slices of bf16 as TMA wrote them) into the
+// form above: this warp rows 8 cw .. below `rows`, half a warp per row. back[row]: the row's power of two
+// undone, which the softmax multiplies into its scale.
+__device__ __forceinline__ void scale_query_rows(uint8_t* q, float* back, int rows, int cw, int lane) {
+  const int half = lane >> 4, l = lane & 15;
+#pragma unroll 1
+  for (int r0 = 8 * cw; r0 < min(8 * cw + 8, rows); r0 += 2) {
+    const int row = r0 + half;
+    // chunks l + 16 i of the row's 72 (slice, chunk): i < 4 latent, i = 4 (l < 8) RoPE
+    uint4 v[5];
+    uint32_t top = 0;  // largest magnitude: bf16 bits order like the values
+#pragma unroll
+    for (int i = 0; i < 5; ++i) {
+      v[i] = make_uint4(0, 0, 0, 0);
+      if (i < 4 || l < 8) v[i] = *reinterpret_cast<const uint4*>(q + (2 * i + (l >> 3)) * 8192 + row * 128 + 16 * (l & 7));
+      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) top = max(top, max(w[j] & 0x7FFFu, (w[j] >> 16) & 0x7FFFu));
+    }
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    // 2^e with e = 11 - exponent(top), kept where 2^e and 2^-e are normal floats
+    const int e = top == 0 ? 0 : max(-100, min(100, 138 - (int)(top >> 7)));
+    const float f = __uint_as_float((uint32_t)(127 + e) << 23);
+    if (l == 0) back[row] = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+    for (int i = 0; i < 5; ++i) {
+      if (i == 4 && l >= 8) break;
+      uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[j]));
+        w[j] = i < 4 ? pack_f16x2(x.x * f, x.y * f) : pack_bf16x2(x.x * f, x.y * f);
+      }
+      *reinterpret_cast<uint4*>(q + (2 * i + (l >> 3)) * 8192 + row * 128 + 16 * (l & 7)) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
 }
 
 // Scores of 32 keys: those whose bit of `valid` is clear become -inf. Most
@@ -184,7 +186,7 @@ __device__ __forceinline__ void mask_scores(uint32_t (&sv)[32], uint32_t valid) 
 // One warp resolves the rows of every step of the part, up to kRowDepth steps
 // ahead of the slowest reader. `wait(bar, parity)` is the kernel's bounded wait.
 template <bool PAIR, bool SPARSE, class Wait>
-__device__ __forceinline__ void row_warp(const DecodeParams& p, PieceIter it, RowTable* rt, int lane, Wait wait) {
+__device__ __forceinline__ void row_warp(const DecodeParams& p, PieceIter it, RowTable* rt, int lane, int rank, Wait wait) {
   constexpr int kTok = PAIR ? 256 : 128;
   Piece pc;
   int gs = 0;
@@ -210,6 +212,18 @@ __device__ __forceinline__ void row_warp(const DecodeParams& p, PieceIter it, Ro
           else row = page_of(p, req, t / kPage, npg) * kPage + t % kPage;
         }
         rt->row[d][32 * w + lane] = row;
+        // the copies find the records in L2: whole pages, or a token's four lines
+        const uint8_t* rec = static_cast<const uint8_t*>(p.kcache) + (size_t)(row >= 0 ? row : 0) * kFp4RecordBytes;
+        if (!PAIR || (w >> 2) == rank) {
+          if (SPARSE) {
+            if (row >= 0) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) asm volatile("prefetch.global.L2 [%0];" ::"l"(rec + min(128 * i, kFp4RecordBytes - 1)));
+            }
+          } else if (lane == 0 && !(w & 1) && row >= 0) {
+            prefetch_l2(rec, min(kPage, Ls - t) * kFp4RecordBytes);
+          }
+        }
         if (SPARSE) {
           const uint32_t m = __ballot_sync(0xffffffffu, row >= 0);
           if (lane == 0) rt->valid[d][w] = m;
@@ -221,134 +235,158 @@ __device__ __forceinline__ void row_warp(const DecodeParams& p, PieceIter it, Ro
   }
 }
 
-// ---------------------------------------------------------------- converters
-// Fills the ring. Two groups of four warps take a phase's latent entries in
-// turn (group g: entries g and g + 2) and its RoPE slice every other step. A
-// thread converts four items of 32 codes per entry: tokens 32 w + 8 j +
-// lane % 8, quarter lane / 8 of the entry's 128 dims; eight neighbouring lanes
-// write the same chunk of eight rows, which the swizzle spreads over all banks.
-// Entry e of a phase: K, and a single CTA's V: latent dims 128 e .. of the
+// Lane 0 waits for the warp (the first try is made by all lanes).
+template <class Wait>
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int lane, Wait wait) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  bool ok = true;
+  if (lane == 0) ok = wait(bar, parity);
+  return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+}
+
+// Entry e of a phase. K, and a single CTA's V: latent dims 128 e .. of the
 // step's (own) tile; a pair's V: tile e / 2, value dims 256 (e % 2) + 128 rank ..
-// `stage`: 16 bytes per item and thread.
-// Scales: lane quarter q loads the eight scale bytes of entry q for its
-// token, and an entry's are handed round by shuffle: one request a phase.
-// The RoPE slice goes straight into its entry with cp.async, whose completion
-// the entry's barrier counts.
-// wait(bar, parity): the kernel's bounded wait; full(slot): the entry's barrier.
-template <bool PAIR, class Wait, class Full>
-__device__ __forceinline__ void convert_ring(const DecodeParams& p, const PieceIter& it, RowTable* rt, uint8_t* ring,
-                                             uint4* stage, uint64_t* empty, int cw, int lane, int rank, Wait wait,
-                                             Full full) {
-  static_assert(kGroups == 2, "two entries per group and phase");
+template <bool PAIR>
+__device__ __forceinline__ int entry_token(bool k, int e, int rank) {
+  return PAIR ? 128 * (k ? rank : e >> 1) : 0;
+}
+template <bool PAIR>
+__device__ __forceinline__ int entry_dim(bool k, int e, int rank) {
+  return PAIR && !k ? 256 * (e & 1) + 128 * rank : 128 * e;
+}
+
+// ---------------------------------------------------------------- loaders
+// Four warps copy the raw bytes of the entries in order: warp w the 32 tokens
+// 32 w .., four lanes on the 64 code bytes of a token, one on its 8 scale bytes.
+template <bool PAIR, class Wait>
+__device__ __forceinline__ void load_raw(const DecodeParams& p, const PieceIter& it, RowTable* rt, uint8_t* raw, int w,
+                                         int lane, int rank, Wait wait) {
   const uint8_t* cache = static_cast<const uint8_t*>(p.kcache);
-  const int grp = cw >> 2, w = cw & 3;
-  const int tok = 32 * w + (lane & 7), q = lane >> 3;
-  const int k0 = PAIR ? 128 * rank : 0;  // first token of this CTA's K tile
-  stage += 32 * cw + lane;
-  auto record = [&](bool k, int step, int e, int j) {
-    return rt->row[step % kRowDepth][(k ? k0 : PAIR ? 128 * (e >> 1) : 0) + tok + 8 * j];
-  };
-  auto dim_of = [&](bool k, int e) { return PAIR && !k ? 256 * (e & 1) + 128 * rank : 128 * e; };
-  auto fetch = [&](bool k, int step, int e) {
-    const int off = dim_of(k, e) / 2 + 16 * q;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int row = record(k, step, e, j);
-      cp_async16(stage + j * (32 * kCvWarps), cache + (size_t)(row >= 0 ? row : 0) * kFp4RecordBytes + off,
-                 row >= 0 ? 16u : 0u);
-    }
-    cp_async_commit();
-  };
-  auto scales = [&](bool k, int step, uint2 (&sc)[4]) {
-    const int off = kFp4ScaleOff + dim_of(k, q) / 16;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int row = record(k, step, q, j);
-      sc[j] = make_uint2(0, 0);
-      if (row >= 0) sc[j] = ldg8(cache + (size_t)row * kFp4RecordBytes + off);
-    }
-  };
-  auto wait_warp = [&](uint64_t* bar, uint32_t parity) {
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-    bool ok = true;
-    if (lane == 0) ok = wait(bar, parity);
-    return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-  };
-  Phases<PAIR> nxt;     // the phase after the one being converted
-  nxt.it = it;
-  uint2 pre[4];         // its scales
-  RingPos pos;          // first entry of the phase being converted
-  bool have = nxt.next();
-  if (have) {
-    if (!wait_warp(&rt->full[0], 0)) return;
-    scales(true, 0, pre);
-    fetch(true, 0, grp);
-  }
+  Phases<PAIR> ph;
+  ph.it = it;
+  uint32_t n = 0;
   bool stop = false;
-  while (have && !stop) {
-    const bool k = nxt.is_k();
-    const int step = nxt.step();
-    have = nxt.next();
-    const bool nk = have && nxt.is_k();
-    const int nstep = nxt.step();
-    if (nk && !wait_warp(&rt->full[nstep % kRowDepth], (nstep / kRowDepth) & 1)) break;
-    // one wait for all scales: loads share a few scoreboards, so one used
-    // while younger loads are in flight would wait for those too
-    uint2 sc[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) sc[j] = make_uint2(settle(pre[j].x), settle(pre[j].y));
-    if (have) scales(nk, nstep, pre);
-    // not unrolled: the unrolled code left no room in the instruction cache
-    // for the other roles
+  while (!stop && ph.next()) {
+    const bool k = ph.is_k();
+    const int step = ph.step(), d = step % kRowDepth;
+    if (k && !wait_warp(&rt->full[d], (step / kRowDepth) & 1, lane, wait)) break;
 #pragma unroll 1
-    for (int e = grp; e < 4; e += 2) {
-      const RingPos at = pos.at(e);
-      cp_async_wait<0>();
-      uint4 codes[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) codes[j] = stage[j * (32 * kCvWarps)];
-      if (e < 2) fetch(k, step, e + 2);
-      else if (have) fetch(nk, nstep, grp);
-      if (!wait_warp(&empty[at.slot], at.parity ^ 1u)) { stop = true; break; }
-      uint8_t* s = ring + at.slot * kSlot + (q >> 1) * kSlice;
+    for (int e = 0; e < 4; ++e, ++n) {
+      const int r = n % kRaw;
+      if (!wait_warp(&rt->raw_empty[r], ((n / kRaw) & 1) ^ 1, lane, wait)) { stop = true; break; }
+      const int32_t* rows = rt->row[d] + entry_token<PAIR>(k, e, rank) + 32 * w;
+      const int d0 = entry_dim<PAIR>(k, e, rank);
+      uint8_t* buf = raw + r * kRawBytes;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint32_t lo = __shfl_sync(0xffffffffu, sc[j].x, 8 * e + (lane & 7));
-        const uint32_t hi = __shfl_sync(0xffffffffu, sc[j].y, 8 * e + (lane & 7));
-        store_item(codes[j], (q & 2 ? hi : lo) >> (16 * (q & 1)), s, tok + 8 * j, 4 * (q & 1));
+        const int row = rows[8 * j + (lane & 7)];
+        cp_async16(buf + ((4 * w + j) * 32 + lane) * 16,
+                   cache + (size_t)(row >= 0 ? row : 0) * kFp4RecordBytes + d0 / 2 + 16 * (lane >> 3), row >= 0 ? 16u : 0u);
       }
+      const int row = rows[lane];
+      cp_async8(buf + 8192 + (32 * w + lane) * 8,
+                cache + (size_t)(row >= 0 ? row : 0) * kFp4RecordBytes + kFp4ScaleOff + d0 / 16, row >= 0 ? 8u : 0u);
+      cp_async_mbar_arrive_noinc(&rt->raw_full[r]);
+    }
+    if (!stop && !k) {  // a step's rows are last read by its V phase
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&rt->empty[d]);
+    }
+  }
+  cp_async_wait<0>();  // no copy may land after the CTA has finished
+}
+
+// ---------------------------------------------------------------- RoPE
+// One warp copies the RoPE slice of every K phase straight into its ring entry,
+// 8 lanes per 128-byte row. The entry's barrier counts the copies and, in the
+// place of a converter group's four warps, four arrivals. This warp uses one
+// entry in nine, so it cannot wait on the entry's own `empty` barrier, whose
+// parity would repeat in between: the MMA issuer commits the phase's entry 1,
+// the previous user of the RoPE slice's place (kN = 3 entries before entry 4),
+// to `free` as well, once per K phase.
+template <bool PAIR, class Wait, class Full>
+__device__ __forceinline__ void load_rope(const DecodeParams& p, const PieceIter& it, RowTable* rt, uint8_t* ring,
+                                          uint64_t* free, int lane, int rank, Wait wait, Full full) {
+  static_assert(kN == 3, "entry 4 takes the place of entry 1");
+  const uint8_t* cache = static_cast<const uint8_t*>(p.kcache) + kFp4RopeOff + 16 * (lane & 7);
+  Phases<PAIR> ph;
+  ph.it = it;
+  RingPos pos;
+  while (ph.next()) {
+    pos.advance(4);
+    if (!ph.is_k()) continue;
+    const int step = ph.step(), d = step % kRowDepth;
+    if (!wait_warp(&rt->full[d], (step / kRowDepth) & 1, lane, wait)) break;
+    // rows first: nothing but the copies is left to do once the place is free
+    const int32_t* rows = rt->row[d] + entry_token<PAIR>(true, 0, rank) + (lane >> 3);
+    int row[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) row[i] = rows[4 * i];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&rt->empty[d]);
+    if (!wait_warp(free, step & 1, lane, wait)) break;
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      cp_async16(sw128(ring + pos.slot * kSlot, 4 * i + (lane >> 3), lane & 7),
+                 cache + (size_t)(row[i] >= 0 ? row[i] : 0) * kFp4RecordBytes, row[i] >= 0 ? 16u : 0u);
+    cp_async_mbar_arrive(full(pos.slot));
+    __syncwarp();
+    if (lane < 4) mbar_arrive(full(pos.slot));
+    pos.advance(1);
+  }
+  cp_async_wait<0>();  // no copy may land after the CTA has finished
+}
+
+// ---------------------------------------------------------------- converters
+// Group g of four warps converts latent entries g and g + 2 of every phase. A
+// thread converts four items of 32 codes: tokens 32 w + 8 j + lane % 8, quarter
+// lane / 8 of the entry's 128 dims; eight neighbouring lanes write the same
+// chunk of eight rows, which the swizzle spreads over all banks. A group's
+// entries are at most kN apart, so its waits on `empty` miss no phase. The raw bytes
+// are taken into registers first, so that the next entry's copies overlap the
+// conversion.
+// Before the first entry of a piece all eight warps bring its query into form:
+// by then the ring has made sure that the piece before is done with its own.
+// wait(bar, parity): the kernel's bounded wait; full(slot): the entry's barrier;
+// query(piece): waits for the piece's query and brings this warp's rows into form.
+template <bool PAIR, class Wait, class Full, class Query>
+__device__ __forceinline__ void convert_ring(const PieceIter& it, RowTable* rt, uint8_t* ring, const uint8_t* raw,
+                                             uint64_t* empty, int cw, int lane, Wait wait, Full full, Query query) {
+  static_assert(kGroups == 2 && kRaw == 2, "each group has the raw buffer of its number");
+  const int grp = cw >> 2, w = cw & 3;
+  const int tok = 32 * w + (lane & 7), q = lane >> 3;
+  const uint8_t* buf = raw + grp * kRawBytes;
+  Phases<PAIR> ph;
+  ph.it = it;
+  RingPos pos;        // first entry of the phase
+  uint32_t use = 0;   // uses of the raw buffer
+  int piece = 0;
+  bool stop = false;
+  while (!stop && ph.next()) {
+    if (ph.h == 0 && !query(piece++)) break;
+#pragma unroll 1
+    for (int e = grp; e < 4; e += 2, ++use) {
+      const RingPos at = pos.at(e);
+      if (!wait_warp(&rt->raw_full[grp], use & 1, lane, wait)) { stop = true; break; }
+      uint4 codes[4];
+      uint32_t sc[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        codes[j] = *reinterpret_cast<const uint4*>(buf + ((4 * w + j) * 32 + lane) * 16);
+        sc[j] = *reinterpret_cast<const uint16_t*>(buf + 8192 + (tok + 8 * j) * 8 + 2 * q);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&rt->raw_empty[grp]);
+      if (!wait_warp(&empty[at.slot], at.parity ^ 1u, lane, wait)) { stop = true; break; }
+      uint8_t* s = ring + at.slot * kSlot + (q >> 1) * kSlice;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) store_item(codes[j], sc[j], s, tok + 8 * j, 4 * (q & 1));
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(full(at.slot));
     }
-    if (stop) break;
-    if (k) {
-      if (grp == (step & 1)) {  // RoPE slice: 8 lanes per 128-byte row
-        const RingPos at = pos.at(4);
-        if (!wait_warp(&empty[at.slot], at.parity ^ 1u)) break;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int t = 32 * w + 4 * i + (lane >> 3), ch = lane & 7;
-          const int row = rt->row[step % kRowDepth][k0 + t];
-          cp_async16(sw128(ring + at.slot * kSlot, t, ch),
-                     cache + (size_t)(row >= 0 ? row : 0) * kFp4RecordBytes + kFp4RopeOff + 16 * ch, row >= 0 ? 16u : 0u);
-        }
-        cp_async_mbar_arrive(full(at.slot));
-        __syncwarp();
-        if (lane == 0) mbar_arrive(full(at.slot));
-      }
-      pos.advance(5);
-    } else {
-      pos.advance(4);
-    }
-    // the rows of a step are last read by the fetches of its V phase: the one
-    // of entry grp + 2 is issued in that phase itself
-    if (!k) {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&rt->empty[step % kRowDepth]);
-    }
+    pos.advance(ph.is_k() ? 5 : 4);
   }
-  cp_async_wait<0>();  // no copy may land after the CTA has finished
 }
 
 }  // namespace fp4
