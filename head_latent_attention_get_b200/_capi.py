@@ -118,10 +118,18 @@ def _ptr(t):
     return t.data_ptr()
 
 
+_raw_stream = None
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the raw handle: building a torch.cuda.Stream costs more than a small kernel
+        global _raw_stream
+        if _raw_stream is None:
+            import torch
+            torch.cuda.current_stream()  # initialises CUDA
+            _raw_stream = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+        return _raw_stream[0](_raw_stream[1]())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
