@@ -78,6 +78,37 @@ __device__ __forceinline__ bool group_sync(Ctrl* c, uint64_t* bar, uint32_t& pha
   return ok;
 }
 
+__device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void put(float* p, float v) { *p = v; }
+
+// O^T (value dims 128 m + the thread's on TMEM lanes, rows on columns) times
+// the rows' factors -> the rows below `rows`, kDv apart, at dst + 128 m.
+template <int NR, typename T>
+__device__ __forceinline__ void store_rows(T* dst, uint32_t taddr, const float* inv_l, int rows) {
+#pragma unroll 1
+  for (int c16 = 0; c16 < NR / 16; ++c16, dst += 16 * kDv) {
+    const int n = rows - 16 * c16;
+    if (n <= 0) break;
+    float f[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) f[i] = inv_l[16 * c16 + i];
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      uint32_t ov[16];
+      tmem_ld16(taddr + 64 * m + 16 * c16, ov);
+      tmem_ld_wait();
+      if (n >= 16) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) put(dst + i * kDv + 128 * m, __uint_as_float(ov[i]) * f[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (i < n) put(dst + i * kDv + 128 * m, __uint_as_float(ov[i]) * f[i]);
+      }
+    }
+  }
+}
+
 template <int NR, bool SPARSE>
 __global__ void __launch_bounds__(fp4::kThreads, 1)
     mla_decode_fp4_kernel(const __grid_constant__ CUtensorMap tm_q, const DecodeParams p) {
@@ -385,28 +416,11 @@ __global__ void __launch_bounds__(fp4::kThreads, 1)
         }
       }
       if (!group_sync(c, &c->grp_sm, gph, p)) { stop = true; break; }
-#pragma unroll 1
-      for (int m = 0; m < 4; ++m) {
-        const int d = 128 * m + 32 * q4 + lane;
-#pragma unroll 1
-        for (int c16 = 0; c16 < NR / 16; ++c16) {
-          uint32_t ov[16];
-          tmem_ld16(tmem + lane_base + 64 * m + 16 * c16, ov);
-          tmem_ld_wait();
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int rr = 16 * c16 + i;
-            if (rr < rows_here) {
-              const float val = __uint_as_float(ov[i]) * c->inv_l[rr];
-              if (pc.single)
-                static_cast<__nv_bfloat16*>(p.out)[((size_t)pc.unit * p.rows + row0 + rr) * kDv + d] =
-                    __float2bfloat16_rn(val);
-              else
-                p.ws_o[((size_t)pc.ws_idx * p.rows + row0 + rr) * kDv + d] = val;
-            }
-          }
-        }
-      }
+      // one pointer per piece and constant offsets from it: with the address and
+      // the kind of output worked out per element this took 20 us a piece
+      const size_t row_at = (size_t)(pc.single ? pc.unit : pc.ws_idx) * p.rows * kDv + 32 * q4 + lane;
+      if (pc.single) store_rows<NR>(static_cast<__nv_bfloat16*>(p.out) + row_at, tmem + lane_base, c->inv_l, rows_here);
+      else store_rows<NR>(p.ws_o + row_at, tmem + lane_base, c->inv_l, rows_here);
       tc_fence_before();
       if (!group_sync(c, &c->grp_sm, gph, p)) { stop = true; break; }
       mbar_arrive(&c->o_free);
