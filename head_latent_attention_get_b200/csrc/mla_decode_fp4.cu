@@ -277,8 +277,10 @@ __global__ void __launch_bounds__(fp4::kThreads, 1)
     while (!stop && it.next(pc)) {
       const int req = unit_req(p, pc.unit);
       const int grow = row0 + r;                          // row within the unit
-      int limit = 0;
-      if (!SPARSE) {
+      // lanes without a row are not masked at all: what they compute is not read,
+      // and a full word costs the whole warp one comparison (mask_scores)
+      int limit = 0x7fffffff;
+      if (!SPARSE && rvalid) {
         const int Ls = p.seqlens[req];
         limit = Ls;
         if (p.causal) limit = Ls - p.s_q + row_query(p, pc.unit, grow) + 1;
@@ -303,7 +305,6 @@ __global__ void __launch_bounds__(fp4::kThreads, 1)
           };
           vmask = make_uint4(word(0), word(1), word(2), word(3));
         }
-        if (!rvalid) vmask = make_uint4(0, 0, 0, 0);
         if (!timed_wait(c, &c->s_full[b], (gt >> 1) & 1, p)) { stop = true; break; }
         tc_fence_after();
         if (k == pc.t0) scale_log2 = p.scale_log2 * c->q_back[pi & 1][r & 63];
@@ -324,7 +325,7 @@ __global__ void __launch_bounds__(fp4::kThreads, 1)
         if ((tmax - m_used) * scale_log2 > kRescaleLog2) {  // also for the first keys; never for -inf - -inf
           const float m_new = tmax;
           alpha = (m_used == -INFINITY) ? 0.f : ex2_approx((m_used - m_new) * scale_log2);
-          need = (k != pc.t0) && (m_used != -INFINITY);
+          need = rvalid && (k != pc.t0) && (m_used != -INFINITY);
           m_used = m_new;
           l_sum *= alpha;
         }
