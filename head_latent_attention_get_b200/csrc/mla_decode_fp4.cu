@@ -331,8 +331,8 @@ __global__ void __launch_bounds__(fp4::kThreads, 1)
         }
         // pass 2: probabilities (a masked score is -inf: e^-inf = 0) -> f16, staged
         // in TMEM over the S columns already read (tokens 32w.. -> columns 16w..)
-        const float mc = (m_used == -INFINITY ? 0.f : m_used) * scale_log2;
-        float part = 0.f;
+        const float mc = m_used == -INFINITY ? 0.f : m_used;
+        uint64_t sum = join2(0.f, 0.f);
 #pragma unroll 1
         for (int w = 0; w < 4; ++w) {
           uint32_t sv[32];
@@ -340,17 +340,13 @@ __global__ void __launch_bounds__(fp4::kThreads, 1)
           tmem_ld_wait();
           fp4::mask_scores(sv, pick4u(vmask, w));
           uint32_t pk[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float p0 = ex2_approx(fmaf(__uint_as_float(sv[2 * i]), scale_log2, -mc));
-            const float p1 = ex2_approx(fmaf(__uint_as_float(sv[2 * i + 1]), scale_log2, -mc));
-            pk[i] = pack_f16x2(p0, p1);
-            part += p0 + p1;
-          }
+          fp4::probabilities(sv, mc, scale_log2, pk, sum);
           tmem_st16(s_addr + 16 * w, pk);
         }
         tmem_st_wait();
-        l_sum += part;
+        float even, odd;
+        split2(sum, even, odd);
+        l_sum += even + odd;
         if (owner) c->alpha[r] = alpha;
         if (need) c->rescale_flag[gt & 1] = 1;
         if (!group_sync(c, &c->grp_sm, gph, p)) { stop = true; break; }

@@ -351,20 +351,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
         // the next completion of the same barrier, needs this thread's P, so
         // the parity wait never falls two phases behind.) The first
         // quarter is computed into registers while that product runs.
-        const float mc = (m_used == -INFINITY ? 0.f : m_used) * scale_log2;
-        float part = 0.f;
+        const float mc = m_used == -INFINITY ? 0.f : m_used;
+        uint64_t sum = join2(0.f, 0.f);
         auto probs = [&](int w, uint32_t (&pk)[16]) {
           uint32_t sv[32];
           tmem_ld32(s_addr + 32 * w, sv);
           tmem_ld_wait();
           fp4::mask_scores(sv, pick4u(vm, w));
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float p0 = ex2_approx(fmaf(__uint_as_float(sv[2 * i]), scale_log2, -mc));
-            const float p1 = ex2_approx(fmaf(__uint_as_float(sv[2 * i + 1]), scale_log2, -mc));
-            pk[i] = pack_f16x2(p0, p1);
-            part += p0 + p1;
-          }
+          fp4::probabilities(sv, mc, scale_log2, pk, sum);
         };
         auto store = [&](int w, const uint32_t (&pk)[16]) {
           uint8_t* rowp = sP + (2 * half + (w >> 1)) * 8192 + (row >> 3) * 1024 + (row & 7) * 128;
@@ -385,7 +379,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
           store(w, pk);
         }
         tc_fence_after();
-        l_sum += part;
+        float even, odd;
+        split2(sum, even, odd);
+        l_sum += even + odd;
         if (need) {
           // O holds every product up to step gt - 1 (waited for above)
 #pragma unroll 1

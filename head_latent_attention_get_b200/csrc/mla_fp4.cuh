@@ -182,6 +182,24 @@ __device__ __forceinline__ void mask_scores(uint32_t (&sv)[32], uint32_t valid) 
     if (!((valid >> i) & 1u)) sv[i] = 0xff800000u;
 }
 
+// Probabilities of 32 keys from their scores: 2^((s - m) * scale_log2), as f16
+// pairs, and their sums added to `sum` (even and odd keys). The difference is
+// taken first: a product rounded before it would be off by more than 1 for
+// scores past 2^24. A masked score is -inf: e^-inf = 0.
+__device__ __forceinline__ void probabilities(const uint32_t (&sv)[32], float m, float scale_log2, uint32_t (&pk)[16],
+                                              uint64_t& sum) {
+  const uint64_t nm = join2(-m, -m), sl = join2(scale_log2, scale_log2);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    float x0, x1;
+    split2(mul2(add2(join2(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1])), nm), sl), x0, x1);
+    x0 = ex2_approx(x0);
+    x1 = ex2_approx(x1);
+    pk[i] = pack_f16x2(x0, x1);
+    sum = add2(sum, join2(x0, x1));
+  }
+}
+
 // ---------------------------------------------------------------- row warp
 // One warp resolves the rows of every step of the part, up to kRowDepth steps
 // ahead of the slowest reader. `wait(bar, parity)` is the kernel's bounded wait.

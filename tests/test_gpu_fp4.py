@@ -190,3 +190,71 @@ def test_graph_replay_with_new_lengths(h_q):
 @pytest.mark.parametrize("h_q", [16, 128])
 def test_long_context(h_q):
     _check(_w(batch=1, h_q=h_q, seqlens=[131072], seed=105), few=False)
+
+
+@pytest.mark.parametrize("h_q,topk", [(16, 0), (128, 0), (16, 64), (128, 64)])
+def test_cache_beyond_4_gib(h_q, topk):
+    """Pages past the cache's first 2^32 bytes, through the append and both
+    decode kernels: the same results as for a small cache with the same rows."""
+    w = _w(batch=2, h_q=h_q, seqlens=[200, 129], topk=topk, seed=107)
+    inp = W.make_inputs(w, poison_tail=True)
+    out, lse, _ = G.run_gpu(inp)
+    pages = (1 << 32) // (64 * 416) + 64
+    big = torch.empty(pages, 64, 416, dtype=torch.uint8, device="cuda")
+    shift = pages - inp.num_pages
+    big[shift:].copy_(inp.kcache)
+    moved = dataclasses.replace(inp, block_table=torch.where(inp.block_table >= 0, inp.block_table + shift, inp.block_table))
+    d = G.to_device(dataclasses.replace(moved, kcache=inp.kcache[:1]))
+    d["kcache"] = big
+    out2, lse2, r = G.run_gpu(moved, dev_inputs=d)
+    assert r.status() == (M.MLA_OK, 0)
+    assert np.array_equal(out, out2) and np.array_equal(lse, lse2)
+    kv = torch.randn(3, 576, device="cuda").bfloat16()
+    last = torch.tensor([pages * 64 - 1, 0, pages * 64 - 66], dtype=torch.int32, device="cuda")
+    small = torch.zeros(2, 64, 416, dtype=torch.uint8, device="cuda")
+    M.mla_kv_append(kv, 576, 3, 576, None, 0.0, None, None, last, big, None, M.MLA_KV_FP4_E2M1, pages)
+    M.mla_kv_append(kv, 576, 3, 576, None, 0.0, None, None, torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda"), small,
+                    None, M.MLA_KV_FP4_E2M1, 2)
+    torch.cuda.synchronize()
+    assert torch.equal(big.view(-1, 416)[last.long()], small.view(-1, 416)[:3])
+
+
+def test_two_decodes_at_once():
+    """Two decodes on two streams, each with its own workspace."""
+    runs = []
+    for h_q, seed in ((16, 111), (128, 113)):
+        w = _w(batch=6, h_q=h_q, seqlens=[3000, 129, 64, 2500, 1, 700], seed=seed)
+        d = G.to_device(W.make_inputs(w, poison_tail=True))
+        r = M.DecodeRunner(d["q"], d["kcache"], d["block_table"], d["cache_seqlens"], softmax_scale=w.scale)
+        r.plan()
+        alone = [t.clone() for t in r.run()]
+        runs.append((r, alone, torch.cuda.Stream(), d))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for r, _, s, _ in runs:
+            r.plan(s)
+            r.run(s)
+    torch.cuda.synchronize()
+    for r, alone, _, _ in runs:
+        assert torch.equal(r.out, alone[0]) and torch.equal(r.lse, alone[1])
+
+
+def test_queries_of_any_magnitude():
+    """A row's query is scaled by a power of two on its way to the tensor core:
+    rows from 2^-100 to 2^12 times a common one, and a zero row, with the scale
+    undone by softmax_scale for one of them at a time."""
+    w = _w(batch=1, h_q=16, seqlens=[300], seed=115)
+    inp = W.make_inputs(w)
+    base = inp.q[0, 0, :1].clone()
+    for i in range(16):
+        inp.q[0, 0, i] = (base.float() * 2.0 ** (12 - 7 * i)).to(torch.bfloat16)
+    inp.q[0, 0, 15] = 0
+    for scale in (w.scale, w.scale * 2.0 ** 9, w.scale * 2.0 ** 86):
+        sub = dataclasses.replace(inp, workload=dataclasses.replace(w, scale=scale))
+        out, lse, _ = G.run_gpu(sub)
+        ref_o, ref_l = O.reference_decode(sub)
+        # rows whose scores are spread over thousands are a maximum; fp32 scores are off by 2^-20 of the largest one
+        tol = 2.0 ** -20 * np.abs(ref_l)
+        assert np.all(np.abs(lse - ref_l) <= G.LSE_ATOL + tol)
+        tame = tol[..., None] < 1e-4
+        assert np.all(np.abs(out - ref_o) * tame <= G.OUT_ATOL + 2.0 ** -8 * np.abs(ref_o))
