@@ -4,8 +4,9 @@
 //
 //   y    = latent * (1 / sqrt(mean(latent^2) + eps)) * gamma      (norm)
 //   bf16 = RNE(y), the rotated pairs RNE(x0 c - x1 s), RNE(x0 s + x1 c)
-//   FP8  per 128 values: scale = amax / 448 (1 if amax = 0), code = RNE(x / scale)
-//   FP4  per 16 values:  scale = e4m3(amax / 6),             code = RNE(x / scale)
+//   FP8  per 128 values: scale = amax * (1 / 448) (1 if amax = 0), code = RNE(x / scale)
+//   FP4  per 16 values:  scale = e4m3(amax * (1 / 6)),             code = RNE(x / scale)
+// (1 / 448 and 1 / 6 rounded to fp32)
 //
 // A row map bound by HBM: 1152 bytes in, 416 out per token for 4-bit records.
 // One warp per token: lane l holds latent values 8l..8l+7 and 256+8l.. (an FP4
@@ -142,7 +143,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendParams 
     for (int h = 0; h < 2; ++h) {
 #pragma unroll
       for (int o = 1; o < 16; o <<= 1) amax[h] = fmaxf(amax[h], __shfl_xor_sync(0xffffffffu, amax[h], o));
-      const float scale = amax[h] > 0.f ? __fdiv_rn(amax[h], 448.f) : 1.f;
+      const float scale = amax[h] > 0.f ? __fmul_rn(amax[h], 1.f / 448.f) : 1.f;
       uint32_t pk[2] = {0, 0};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -164,7 +165,7 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendParams 
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       amax[h] = fmaxf(amax[h], __shfl_xor_sync(0xffffffffu, amax[h], 1));
-      const __nv_fp8_storage_t sc = __nv_cvt_float_to_fp8(__fdiv_rn(amax[h], 6.f), __NV_SATFINITE, __NV_E4M3);
+      const __nv_fp8_storage_t sc = __nv_cvt_float_to_fp8(__fmul_rn(amax[h], 1.f / 6.f), __NV_SATFINITE, __NV_E4M3);
       const __half_raw sr = __nv_cvt_fp8_to_halfraw(sc, __NV_E4M3);
       const float sf = __half2float(*reinterpret_cast<const __half*>(&sr));
       const float inv = sf > 0.f ? __fdiv_rn(1.f, sf) : 0.f;

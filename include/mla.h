@@ -384,10 +384,10 @@ mla_status_t mla_extend_tables(const int32_t* context_lens, const int32_t* new_l
  *     values are rotated pair-wise by the token's angles as in mla_q_norm_rope
  *     (512-value rows: after the norm);
  *   - every value is rounded to bf16, and the latent values then to the
- *     cache's format: FP8 per 128 values with scale = amax / 448 (1 if amax is
- *     0), the code of value / scale; E2M1 per 16 values with the UE4M3 scale of
- *     amax / 6, the code of value / scale (0 if the scale rounds to 0); all to
- *     nearest even, saturating;
+ *     cache's format: FP8 per 128 values with scale = amax * (1/448) (1 if amax
+ *     is 0), the code of value / scale; E2M1 per 16 values with the UE4M3 scale
+ *     of amax * (1/6), the code of value / scale (0 if the scale rounds to 0);
+ *     1/448 and 1/6 rounded to fp32, codes to nearest even, saturating;
  *   - the row goes to cache slot slots[t] (page * 64 + token of the page).
  *     -1: the row is skipped; other values outside [0, num_pages * 64) are
  *     skipped and set MLA_DEVICE_STATUS_BOUNDS. Two rows must not name one

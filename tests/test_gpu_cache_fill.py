@@ -184,11 +184,14 @@ def ref_store(row, kv_format):
     if kv_format == M.MLA_KV_BF16:
         return bf(row), None, row.astype(np.float64)
     if kv_format == M.MLA_KV_FP8_E4M3:
-        codes, sc = O.fp8_cast_rows(lat)
+        t = lat.reshape(T, 4, 128)
+        amax = np.abs(t).max(-1)
+        sc = np.where(amax > 0, (amax * (np.float32(1) / np.float32(448))).astype(np.float32), np.float32(1))
+        codes = O.e4m3_encode((t / sc[..., None]).astype(np.float32)).reshape(T, 512)
         rec = np.concatenate([codes, sc.astype(np.float32).view(np.uint8).reshape(T, 16), bf(row[:, 512:])], 1)
         return rec, None, O.dequant_fp8_records(_pad64(rec)).reshape(-1, 576)[:T]
     blk = lat.reshape(T, 32, 16)
-    s8 = O.e4m3_encode((np.abs(blk).max(-1).astype(np.float32) / np.float32(6)).astype(np.float32))
+    s8 = O.e4m3_encode((np.abs(blk).max(-1).astype(np.float32) * (np.float32(1) / np.float32(6))).astype(np.float32))
     s = O.e4m3_to_f64(s8)[..., None]
     q = np.where(s > 0, blk.astype(np.float64) / np.where(s > 0, s, 1), 0.0)
     codes = e2m1_encode(q).reshape(T, 512)
