@@ -222,6 +222,7 @@ __global__ void __launch_bounds__(fp4::kThreads, 1)
             for (int e = 0; e < 5; ++e, pos.advance()) {  // four latent entries of two slices, then RoPE
               const int slot = pos.slot;
               if (!timed_wait(c, &c->full[slot], pos.parity, p)) { stop = true; break; }
+              if (e == 4) fence_proxy_async_smem();  // RoPE comes by cp.async
               tc_fence_after();
               const uint32_t qa = q_lo + 2 * e * (8192 >> 4), kb = k_lo + slot * (fp4::kSlot >> 4);
 #pragma unroll
@@ -307,7 +308,7 @@ __global__ void __launch_bounds__(fp4::kThreads, 1)
         }
         if (!timed_wait(c, &c->s_full[b], (gt >> 1) & 1, p)) { stop = true; break; }
         tc_fence_after();
-        if (k == pc.t0) scale_log2 = p.scale_log2 * c->q_back[pi & 1][r & 63];
+        if (k == pc.t0) scale_log2 = fp4::row_scale(p.scale_log2, c->q_back[pi & 1][r & 63]);
         const uint32_t s_addr = tmem + lane_base + kTmemS + 128 * b;
         // pass 1: tile max
         float tmax = -INFINITY;

@@ -205,9 +205,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
         const int nslots = 9 * fp4::steps_of<true>(pc);  // 5 K and 4 V entries per step
         for (int i = 0; i < nslots; ++i, ++sc) {
           if (!pwait(pr, &c->v_loc[sc % kN], (sc / kN) & 1, p)) { stop = true; break; }
+          // RoPE comes by cp.async: entry 4 of the piece's first K phase, 9, 18, .. of the others
+          if (i == 4 || (i > 0 && i % 9 == 0)) fence_proxy_async_smem();
           // relaxed: a release arrive would wait for memory operations that
           // have nothing to do with the slot; the rows it signals are in
-          // shared memory (each converter fenced them before its arrival)
+          // shared memory and fenced (by each converter before its arrival, or above)
           mbar_arrive_relaxed_cluster(map_to_rank(smem_u32(&c->full[sc % kN]), 0));
         }
       }
@@ -240,6 +242,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
             for (int e = 0; e < 5; ++e, pos.advance()) {  // four latent entries of two slices, then RoPE
               const int slot = pos.slot;
               if (!pwait(pr, &c->full[slot], pos.parity, p)) { stop = true; break; }
+              if (e == 4) fence_proxy_async_smem();  // RoPE comes by cp.async
               tc_fence_after();
               const uint32_t qa = q_lo + 2 * e * (8192 >> 4), kb = k_lo + slot * (fp4::kSlot >> 4);
 #pragma unroll
@@ -318,7 +321,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
         }
         if (!pwait(pr, &c->s_full[b], (gt >> 1) & 1, p)) { stop = true; break; }
         tc_fence_after();
-        if (k == pc.t0) scale_log2 = p.scale_log2 * c->q_back[pi & 1][row];
+        if (k == pc.t0) scale_log2 = fp4::row_scale(p.scale_log2, c->q_back[pi & 1][row]);
         const uint32_t s_addr = tmem + lane_base + kTmemS + 128 * b;
         // pass 1: max over this thread's 128 keys
         float tmax = -INFINITY;

@@ -156,7 +156,7 @@ __device__ __forceinline__ void scale_query_rows(uint8_t* q, float* back, int ro
 #pragma unroll
     for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
     // 2^e with e = 11 - exponent(top), kept where 2^e and 2^-e are normal floats
-    const int e = top == 0 ? 0 : max(-100, min(100, 138 - (int)(top >> 7)));
+    const int e = top == 0 ? 0 : max(-126, min(126, 138 - (int)(top >> 7)));
     const float f = __uint_as_float((uint32_t)(127 + e) << 23);
     if (l == 0) back[row] = __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
@@ -172,6 +172,10 @@ __device__ __forceinline__ void scale_query_rows(uint8_t* q, float* back, int ro
     }
   }
 }
+
+// Factor of a row's raw scores in the exponent. Kept above 0, which would make
+// a masked -inf a NaN; a row that the bound changes has scores below 2^-90.
+__device__ __forceinline__ float row_scale(float scale_log2, float back) { return fmaxf(scale_log2 * back, 0x1p-126f); }
 
 // Scores of 32 keys: those whose bit of `valid` is clear become -inf. Most
 // words are full and cost one comparison.
@@ -336,7 +340,11 @@ __device__ __forceinline__ void load_raw(const DecodeParams& p, const PieceIter&
 // ---------------------------------------------------------------- RoPE
 // One warp copies the RoPE slice of every K phase straight into its ring entry,
 // 8 lanes per 128-byte row. The entry's barrier counts the copies and, in the
-// place of a converter group's four warps, four arrivals. This warp uses one
+// place of a converter group's four warps, four arrivals. cp.async writes like
+// an ordinary store, and who waits for the entry fences it for the tensor core
+// (64 x 128 x 4096 tokens: 124 -> 126 us by that fence in the odd CTA and 122 ->
+// 124 by the issuer's; waiting and fencing here 129; two warps that hold the
+// bytes in registers until the place is free 128, and 64 x 64 x 8192 168 -> 196). This warp uses one
 // entry in nine, so it cannot wait on the entry's own `empty` barrier, whose
 // parity would repeat in between: the MMA issuer commits the phase's entry 1,
 // the previous user of the RoPE slice's place (kN = 3 entries before entry 4),

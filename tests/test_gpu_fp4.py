@@ -258,3 +258,24 @@ def test_queries_of_any_magnitude():
         assert np.all(np.abs(lse - ref_l) <= G.LSE_ATOL + tol)
         tame = tol[..., None] < 1e-4
         assert np.all(np.abs(out - ref_o) * tame <= G.OUT_ATOL + 2.0 ** -8 * np.abs(ref_o))
+
+
+@pytest.mark.parametrize("h_q", [4, 80])
+@pytest.mark.parametrize("row_exp,scale_exp", [((115, 125, 0, -120), -115), ((-120, -126, -90, -120), 120),
+                                               ((-120, -126, 0, -60), -100)])
+def test_queries_at_the_ends_of_the_range(h_q, row_exp, scale_exp):
+    """The largest and the smallest queries that bf16 holds, the rows' power of
+    two undone by softmax_scale, and one so small in total that every score is
+    0: its row is the mean of the values, masked keys still without weight."""
+    w = _w(batch=1, h_q=h_q, seqlens=[300], seed=117)
+    inp = W.make_inputs(w)
+    base = inp.q[0, 0, :1].double().clamp(-4, 4)
+    for i in range(h_q):
+        inp.q[0, 0, i] = (base * 2.0 ** row_exp[i % 4]).to(torch.bfloat16)
+    sub = dataclasses.replace(inp, workload=dataclasses.replace(w, scale=w.scale * 2.0 ** scale_exp))
+    out, lse, _ = G.run_gpu(sub)
+    ref_o, ref_l = O.reference_decode(sub)
+    tol = 2.0 ** -20 * np.abs(ref_l)   # fp32 scores, as above
+    assert np.all(np.abs(lse - ref_l) <= G.LSE_ATOL + tol)
+    tame = tol[..., None] < 1e-4
+    assert np.all(np.abs(out - ref_o) * tame <= G.OUT_ATOL + 2.0 ** -8 * np.abs(ref_o))
