@@ -23,8 +23,8 @@
 //
 // The work is cut by latency: one warp resolves rows, four copy raw bytes, one
 // the RoPE slices, eight only convert (two groups on alternate entries), so no
-// role waits for another's round trips. With the copies in the converter
-// warps an entry took 1.7x as long.
+// role waits for another's round trips (with the raw copies in the converter
+// warps 64 x 64 heads x 8192 tokens took 219 us in place of 205).
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
