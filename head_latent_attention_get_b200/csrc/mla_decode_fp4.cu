@@ -448,8 +448,8 @@ cudaError_t launch_one(const CUtensorMap& tq, const DecodeParams& p, int parts, 
 
 cudaError_t launch_decode_fp4(const CUtensorMap& tq, const DecodeParams& p, int parts, bool sparse,
                               cudaStream_t stream) {
-  // <= 16 rows run in the 32-row kernel: the extra P^T rows are written as
-  // zeros and their output rows are never stored
+  // <= 16 rows run in the 32-row kernel: what the extra rows hold (P^T rows and
+  // O^T columns of their own) is never stored
   if (p.rows <= 32) return sparse ? launch_one<32, true>(tq, p, parts, stream) : launch_one<32, false>(tq, p, parts, stream);
   if (p.rows <= 48) return sparse ? launch_one<48, true>(tq, p, parts, stream) : launch_one<48, false>(tq, p, parts, stream);
   return sparse ? launch_one<64, true>(tq, p, parts, stream) : launch_one<64, false>(tq, p, parts, stream);
