@@ -618,7 +618,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SPARSE ? kThreadsSpa
         }
         tc_fence_after();
         l_sum += part;
-        if (need) {
+        // A warp's rows grow apart, but its tensor-memory accesses are collective:
+        // all of its rows are multiplied as soon as one needs it (alpha is 1 for the others).
+        if (__any_sync(0xffffffffu, need)) {
           // O holds every product up to step gt - 1 (waited for above)
 #pragma unroll 1
           for (int c16 = 0; c16 < 16; ++c16) {  // 2 x 128 columns of this row

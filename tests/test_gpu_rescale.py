@@ -59,7 +59,7 @@ def rescaled_rows(inp, step):
     return np.array(hit)
 
 
-CASES = [(kv, h_q, sparse) for kv in ("fp4",) for h_q in (16, 48, 80, 128) for sparse in (False, True)]
+CASES = [(kv, h_q, sparse) for kv in ("fp4", "bf16", "fp8") for h_q in (16, 48, 80, 128) for sparse in (False, True)]
 
 
 @pytest.mark.parametrize("kv,h_q,sparse", CASES)
