@@ -461,7 +461,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
   }
 
   // ---------------------------------------------------------------- teardown
-  // Every copy of this CTA has landed: the converters and the Q warp waited
+  // Every copy of this CTA has landed: the loader, RoPE and Q warps waited
   // for their own. After an abort a remote arrive or a pair MMA of the other
   // CTA may be pending for microseconds, so the CTA holds its shared memory
   // for a fixed 200 us of wall time (%globaltimer, not a sleep hint that may

@@ -334,7 +334,7 @@ __device__ __forceinline__ void load_raw(const DecodeParams& p, const PieceIter&
       if (lane == 0) mbar_arrive(&rt->empty[d]);
     }
   }
-  cp_async_wait<0>();  // no copy may land after the CTA has finished
+  cp_async_wait_all();  // no copy may land after the CTA has finished, also where a wait above gave up
 }
 
 // ---------------------------------------------------------------- RoPE
@@ -379,7 +379,7 @@ __device__ __forceinline__ void load_rope(const DecodeParams& p, const PieceIter
     if (lane < 4) mbar_arrive(full(pos.slot));
     pos.advance(1);
   }
-  cp_async_wait<0>();  // no copy may land after the CTA has finished
+  cp_async_wait_all();  // no copy may land after the CTA has finished, also where a wait above gave up
 }
 
 // ---------------------------------------------------------------- converters

@@ -1,0 +1,36 @@
+"""A decode that gave up leaves nothing behind: its copies have landed before
+its blocks end, so the next decodes are as if it had not been."""
+import dataclasses
+
+import pytest
+import torch
+
+import head_latent_attention_get_b200 as M
+from tests import gpu_helpers as G
+from workloads import mla_workloads as W
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("h_q", [16, 64, 128])
+@pytest.mark.parametrize("topk", [0, 1024])
+def test_decodes_after_timeouts(h_q, topk):
+    """Scores withheld: the loaders stop with copies in flight, for every part
+    of the grid at once. A good decode follows in the same stream each time."""
+    w = dataclasses.replace(W.get_workload("tiny"), batch=40, s_q=1, h_q=h_q, seqlens=[1500 + 37 * i for i in range(40)], causal=False,
+                            topk=topk, kv="fp4", seed=211)
+    d = G.to_device(W.make_inputs(w, poison_tail=True))
+    make = lambda **kw: M.DecodeRunner(d["q"], d["kcache"], d["block_table"], d["cache_seqlens"], softmax_scale=w.scale,  # noqa: E731
+                                       indices=d["indices"], **kw)
+    good, bad = make(), make(timeout_ns=2_000_000, debug_flags=M.MLA_DEBUG_WITHHOLD_SCORES)
+    good.plan()
+    bad.plan()
+    want = [t.clone() for t in good.run()]
+    for _ in range(5):
+        bad.run()
+        out, lse = good.run()
+        code, bits = bad.status()
+        assert code == M.MLA_ERR_DEVICE_TIMEOUT and bits == M.MLA_DEVICE_STATUS_TIMEOUT
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+        M.mla_clear_device_status(bad.workspace)
+    assert good.status() == (M.MLA_OK, 0)
