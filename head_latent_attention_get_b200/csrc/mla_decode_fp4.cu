@@ -167,6 +167,7 @@ __global__ void __launch_bounds__(fp4::kThreads, 1)
   Piece pc;
   auto wait = [&](uint64_t* bar, uint32_t parity) { return timed_wait(c, bar, parity, p); };
   auto full = [&](int slot) { return &c->full[slot]; };
+  auto arrive = [&](int slot, int) { mbar_arrive(&c->full[slot]); };
 
   if (warp == 0) {
     // ------------------------------------------------------------ Q
@@ -185,11 +186,11 @@ __global__ void __launch_bounds__(fp4::kThreads, 1)
   } else if (warp == 2) {
     fp4::row_warp<false, SPARSE>(p, it, rt, lane, 0, wait);
   } else if (warp == 3) {
-    fp4::load_rope<false>(p, it, rt, sRing, &c->rope_free, lane, 0, wait, full);
+    fp4::load_rope<false>(p, it, rt, sRing, &c->rope_free, lane, 0, wait, full, arrive);
   } else if (warp >= 8 && warp < 12) {
     fp4::load_raw<false>(p, it, rt, sRaw, warp - 8, lane, 0, wait);
   } else if (warp >= 12) {
-    fp4::convert_ring<false>(it, rt, sRing, sRaw, c->empty, warp - 12, lane, wait, full, [&](int piece) {
+    fp4::convert_ring<false>(it, rt, sRing, sRaw, c->empty, warp - 12, lane, wait, arrive, [&](int piece) {
       if (!fp4::wait_warp(&c->q_raw, piece & 1, lane, wait)) return false;
       fp4::scale_query_rows(sQ, c->q_back[piece & 1], rows_here, warp - 12, lane);
       fence_proxy_async_smem();

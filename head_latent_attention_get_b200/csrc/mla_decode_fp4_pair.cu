@@ -38,17 +38,18 @@ constexpr float kRescaleLog2 = 8.0f;
 struct Ctrl {
   // barriers counted on the even CTA (the MMA issuer) ...
   uint64_t q_full;                     // 16 arrivals: both CTAs' converter warps have Q in form
-  uint64_t full[kN];                   // 8 converter warps + 1 forward from the odd CTA
+  uint64_t full[kN];                   // 4 arrivals here and the 4 bytes that the odd CTA's forwarder sends
   uint64_t p_full[2], o_free;          // 8 arrivals: 4 softmax warps x 2 CTAs
   uint64_t drain;
   // ... and in each CTA
   uint64_t q_raw;                      // Q as loaded
   uint64_t q_empty, empty[kN], rope_free;  // pair-MMA commits; rope_free: entry 1 of a K phase
   uint64_t s_full[2], o_done[2];       // pair-MMA commits; o_done[g & 1] completes O of step g
-  uint64_t v_loc[kN];                  // odd CTA: its 8 converter warps
+  uint64_t v_loc[kN];                  // odd CTA: the same 4 arrivals
   uint64_t grp_sm;                     // 128 softmax threads
   float q_back[2][64];                 // [piece parity][row]: what undoes the query's scaling
   uint32_t tmem_base;
+  uint32_t forwarded;                  // where those 4 bytes land; never read
   int abort_flag;
   float mx[2][2][64];                  // [step parity][token half][row]: per-half tile max
   float lx[2][64];                     // [token half][row]: per-half row sum
@@ -128,7 +129,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
   if (threadIdx.x == 0) {
     mbar_init(&c->q_full, 2 * fp4::kCvWarps);
     mbar_init(&c->q_raw, 1);
-    for (int i = 0; i < kN; ++i) mbar_init(&c->full[i], 4 + 1);
+    for (int i = 0; i < kN; ++i) mbar_init(&c->full[i], 4);
     for (int i = 0; i < 2; ++i) mbar_init(&c->p_full[i], 8);
     mbar_init(&c->o_free, 8);
     mbar_init(&c->drain, 1);
@@ -166,6 +167,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
   Piece pc;
   auto wait = [&](uint64_t* bar, uint32_t parity) { return pwait(pr, bar, parity, p); };
   auto full = [&](int slot) { return pr.leader ? &c->full[slot] : &c->v_loc[slot]; };
+  auto arrive = [&](int slot, int w) {  // one of an entry's four arrivals
+    if (pr.leader && w == 0) mbar_arrive_expect_tx(&c->full[slot], 4);
+    else mbar_arrive(full(slot));
+  };
 
   if (warp == 0) {
     // ------------------------------------------------------------ Q
@@ -184,11 +189,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
   } else if (warp == 2) {
     fp4::row_warp<true, SPARSE>(p, it, rt, lane, (int)pr.rank, wait);
   } else if (warp == 3) {
-    fp4::load_rope<true>(p, it, rt, sRing, &c->rope_free, lane, (int)pr.rank, wait, full);
+    fp4::load_rope<true>(p, it, rt, sRing, &c->rope_free, lane, (int)pr.rank, wait, full, arrive);
   } else if (warp >= 8 && warp < 12) {
     fp4::load_raw<true>(p, it, rt, sRaw, warp - 8, lane, (int)pr.rank, wait);
   } else if (warp >= 12) {
-    fp4::convert_ring<true>(it, rt, sRing, sRaw, c->empty, warp - 12, lane, wait, full, [&](int piece) {
+    fp4::convert_ring<true>(it, rt, sRing, sRaw, c->empty, warp - 12, lane, wait, arrive, [&](int piece) {
       if (!fp4::wait_warp(&c->q_raw, piece & 1, lane, wait)) return false;
       fp4::scale_query_rows(sQ, c->q_back[piece & 1], min(64, p.rows - row0), warp - 12, lane);
       fence_proxy_async_smem();
@@ -207,10 +212,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
           if (!pwait(pr, &c->v_loc[sc % kN], (sc / kN) & 1, p)) { stop = true; break; }
           // RoPE comes by cp.async: entry 4 of the piece's first K phase, 9, 18, .. of the others
           if (i == 4 || (i > 0 && i % 9 == 0)) fence_proxy_async_smem();
-          // relaxed: a release arrive would wait for memory operations that
-          // have nothing to do with the slot; the rows it signals are in
-          // shared memory and fenced (by each converter before its arrival, or above)
-          mbar_arrive_relaxed_cluster(map_to_rank(smem_u32(&c->full[sc % kN]), 0));
+          // The rows (acquired from v_loc, fenced by their writers or above) must
+          // come before the even CTA's use of them: the count of an asynchronous
+          // store is a release at cluster scope. 64 x 128 x 4096 tokens, us a call:
+          // 137 (134 with a relaxed arrive, which orders nothing; 144 with
+          // arrive.release.cluster, and 147 with that in the converters themselves)
+          st_async_u32(map_to_rank(smem_u32(&c->forwarded), 0), 0, map_to_rank(smem_u32(&c->full[sc % kN]), 0));
         }
       }
     }

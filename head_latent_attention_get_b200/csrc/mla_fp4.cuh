@@ -349,9 +349,9 @@ __device__ __forceinline__ void load_raw(const DecodeParams& p, const PieceIter&
 // parity would repeat in between: the MMA issuer commits the phase's entry 1,
 // the previous user of the RoPE slice's place (kN = 3 entries before entry 4),
 // to `free` as well, once per K phase.
-template <bool PAIR, class Wait, class Full>
+template <bool PAIR, class Wait, class Full, class Arrive>
 __device__ __forceinline__ void load_rope(const DecodeParams& p, const PieceIter& it, RowTable* rt, uint8_t* ring,
-                                          uint64_t* free, int lane, int rank, Wait wait, Full full) {
+                                          uint64_t* free, int lane, int rank, Wait wait, Full full, Arrive arrive) {
   static_assert(kN == 3, "entry 4 takes the place of entry 1");
   const uint8_t* cache = static_cast<const uint8_t*>(p.kcache) + kFp4RopeOff + 16 * (lane & 7);
   Phases<PAIR> ph;
@@ -376,7 +376,7 @@ __device__ __forceinline__ void load_rope(const DecodeParams& p, const PieceIter
                  cache + (size_t)(row[i] >= 0 ? row[i] : 0) * kFp4RecordBytes, row[i] >= 0 ? 16u : 0u);
     cp_async_mbar_arrive(full(pos.slot));
     __syncwarp();
-    if (lane < 4) mbar_arrive(full(pos.slot));
+    if (lane < 4) arrive(pos.slot, lane);
     pos.advance(1);
   }
   cp_async_wait_all();  // no copy may land after the CTA has finished, also where a wait above gave up
@@ -392,11 +392,11 @@ __device__ __forceinline__ void load_rope(const DecodeParams& p, const PieceIter
 // conversion.
 // Before the first entry of a piece all eight warps bring its query into form:
 // by then the ring has made sure that the piece before is done with its own.
-// wait(bar, parity): the kernel's bounded wait; full(slot): the entry's barrier;
+// wait(bar, parity): the kernel's bounded wait; arrive(slot, w): warp w of four has its part of the entry;
 // query(piece): waits for the piece's query and brings this warp's rows into form.
-template <bool PAIR, class Wait, class Full, class Query>
+template <bool PAIR, class Wait, class Arrive, class Query>
 __device__ __forceinline__ void convert_ring(const PieceIter& it, RowTable* rt, uint8_t* ring, const uint8_t* raw,
-                                             uint64_t* empty, int cw, int lane, Wait wait, Full full, Query query) {
+                                             uint64_t* empty, int cw, int lane, Wait wait, Arrive arrive, Query query) {
   static_assert(kGroups == 2 && kRaw == 2, "each group has the raw buffer of its number");
   const int grp = cw >> 2, w = cw & 3;
   const int tok = 32 * w + (lane & 7), q = lane >> 3;
@@ -428,7 +428,7 @@ __device__ __forceinline__ void convert_ring(const PieceIter& it, RowTable* rt, 
       for (int j = 0; j < 4; ++j) store_item(codes[j], sc[j], s, tok + 8 * j, 4 * (q & 1));
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(full(at.slot));
+      if (lane == 0) arrive(at.slot, w);
     }
     pos.advance(ph.is_k() ? 5 : 4);
   }

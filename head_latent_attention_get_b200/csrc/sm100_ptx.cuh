@@ -280,6 +280,14 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster_addr) {
 __device__ __forceinline__ void mbar_arrive_relaxed_cluster(uint32_t bar_cluster_addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster_addr) : "memory");
 }
+// Writes 4 bytes into another CTA's shared memory and counts them on that CTA's
+// mbarrier. The count has release semantics at cluster scope: what this thread
+// has seen before is visible to who waits for the phase.
+__device__ __forceinline__ void st_async_u32(uint32_t dst_cluster_addr, uint32_t v, uint32_t bar_cluster_addr) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.u32 [%0], %1, [%2];" ::"r"(dst_cluster_addr),
+               "r"(v), "r"(bar_cluster_addr)
+               : "memory");
+}
 // Counts `bytes` of transaction completion on a (possibly remote) mbarrier
 // without arriving. Relaxed: precede it with fence_acq_rel_cluster() when
 // data written by this thread must be visible to the waiter.
