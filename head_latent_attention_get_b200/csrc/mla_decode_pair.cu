@@ -73,7 +73,8 @@ struct Smem {
 struct Ctrl {
   // barriers counted on the even CTA (the MMA issuer) ...
   uint64_t q_full;                     // 1 arrival (+ both CTAs' Q bytes)
-  uint64_t full[kN];                   // 1 arrival (+ both CTAs' bytes of the slot)
+  uint64_t full[kN];                   // 1 arrival (+ both CTAs' bytes of the slot); sparse: 128 loader threads,
+                                       // 1 arrival with the 4 bytes that the odd CTA's forwarder sends
   uint64_t p_full[2], o_free;          // 8 arrivals: 4 softmax warps x 2 CTAs
   uint64_t drain;
   // ... and in each CTA
@@ -84,6 +85,7 @@ struct Ctrl {
   uint64_t v_loc[kN];                  // sparse, odd CTA: its 128 loader threads
   uint64_t grp_sm;                     // 128 softmax threads
   uint32_t tmem_base;
+  uint32_t forwarded;                  // sparse: where the forwarder's words land; never read
   int abort_flag;
   float mx[2][2][64];                  // [step parity][token half][row]: per-half tile max
   float lx[2][64];                     // [token half][row]: per-half row sum
@@ -391,6 +393,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SPARSE ? kThreadsSpa
               cp_async16(base + key * 128 + ((ch ^ (key & 7)) << 4), src, r >= 0 ? 16u : 0u);
             }
             cp_async_commit();
+            if (pr.leader && lw == 0 && lane == 0) mbar_arrive_expect_tx(&c->full[slot], 4);  // the odd CTA's word
             cp_async_mbar_arrive_noinc(pr.leader ? &c->full[slot] : &c->v_loc[slot]);
           }
           ++gk;
@@ -421,6 +424,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SPARSE ? kThreadsSpa
                 }
                 cp_async_commit();
               }
+              if (pr.leader && lw == 0 && lane == 0) mbar_arrive_expect_tx(&c->full[slot], 4);
               cp_async_mbar_arrive_noinc(pr.leader ? &c->full[slot] : &c->v_loc[slot]);
             }
           }
@@ -439,10 +443,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SPARSE ? kThreadsSpa
         const int nslots = 17 * ((pc.t1 - pc.t0 + 1) >> 1);  // 9 K slices + 8 V slots per step
         for (int i = 0; i < nslots; ++i, ++sc) {
           if (!pwait(pr, &c->v_loc[sc % kN], (sc / kN) & 1, p)) { stop = true; break; }
-          // relaxed: a release arrive would first wait for this thread's
-          // earlier memory operations (~0.8K clk after cp.async traffic
-          // instead of ~0.1K); the data it signals has landed (v_loc)
-          mbar_arrive_relaxed_cluster(map_to_rank(smem_u32(&c->full[sc % kN]), 0));
+          // cp.async writes like an ordinary store: fenced for the tensor core here
+          // (the even CTA's by the issuer). The store's count is a release at
+          // cluster scope; an arrive.release.cluster waits for a fence.
+          fence_proxy_async_smem();
+          st_async_u32(map_to_rank(smem_u32(&c->forwarded), 0), 0, map_to_rank(smem_u32(&c->full[sc % kN]), 0));
         }
       }
     }
@@ -469,6 +474,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SPARSE ? kThreadsSpa
             for (int j = 0; j < 9; ++j, ++sc) {
               const int slot = sc % kN;
               if (!pwait(pr, &c->full[slot], (sc / kN) & 1, p)) { stop = true; break; }
+              if (SPARSE) fence_proxy_async_smem();
               tc_fence_after();
               const uint32_t qa = smem_u32(sQ + j * 8192), kb = smem_u32(sRing + slot * kSlot);
 #pragma unroll
@@ -490,6 +496,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SPARSE ? kThreadsSpa
               for (int jd = 0; jd < 2; ++jd, ++sc) {
                 const int slot = sc % kN;
                 if (!pwait(pr, &c->full[slot], (sc / kN) & 1, p)) { stop = true; break; }
+                if (SPARSE) fence_proxy_async_smem();
                 tc_fence_after();
                 const uint32_t va = smem_u32(sRing + slot * kSlot);
 #pragma unroll

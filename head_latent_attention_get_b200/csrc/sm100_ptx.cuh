@@ -273,13 +273,6 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t saddr, uint32_t rank) {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster_addr) : "memory");
 }
-// Remote arrive without release semantics: it does not wait for this
-// thread's earlier memory operations (a release arrive after cp.async traffic
-// costs ~0.8K clk, this one ~0.1K). The caller orders the data it signals by
-// other means (an acquire of its completion, then a proxy fence).
-__device__ __forceinline__ void mbar_arrive_relaxed_cluster(uint32_t bar_cluster_addr) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster_addr) : "memory");
-}
 // Writes 4 bytes into another CTA's shared memory and counts them on that CTA's
 // mbarrier. The count has release semantics at cluster scope: what this thread
 // has seen before is visible to who waits for the phase.
