@@ -157,7 +157,9 @@ mla_status_t run_decode(const mla_decode_args* a, const int32_t* indices, int to
   p.ws_lse = reinterpret_cast<float*>(ws + w.lse_off);
   p.ws_o = reinterpret_cast<float*>(ws + w.o_off);
   p.status = reinterpret_cast<uint32_t*>(ws);
-  p.timeout_ns = a->timeout_ns ? a->timeout_ns : 2000000000ull;
+  // At least 1 ms: a block that gives up still waits, under the same limit, for
+  // the copies and MMAs that it has in flight, and must not end before them.
+  p.timeout_ns = !a->timeout_ns ? 2000000000ull : a->timeout_ns < 1000000ull ? 1000000ull : a->timeout_ns;
   p.debug_flags = a->debug_flags;
   p.sink = a->sink;
   p.q_nvfp4 = static_cast<const uint8_t*>(a->q);

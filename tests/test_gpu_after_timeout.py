@@ -34,3 +34,16 @@ def test_decodes_after_timeouts(h_q, topk):
         assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
         M.mla_clear_device_status(bad.workspace)
     assert good.status() == (M.MLA_OK, 0)
+
+
+@pytest.mark.parametrize("kv,h_q", [("fp4", 16), ("fp4", 128), ("bf16", 16), ("bf16", 128), ("fp8", 64)])
+def test_shortest_limit(kv, h_q):
+    """A limit of 1 ns counts as 1 ms: a block's last waits are for its own
+    copies and MMAs, so no limit may let it end before those. The decode takes
+    microseconds and is not disturbed."""
+    w = dataclasses.replace(W.get_workload("tiny"), batch=6, s_q=1, h_q=h_q, seqlens=[700 + 37 * i for i in range(6)], causal=False, kv=kv,
+                            seed=227)
+    inp = W.make_inputs(w, poison_tail=True)
+    out, lse, r = G.run_gpu(inp, dict(timeout_ns=1))
+    assert r.status() == (M.MLA_OK, 0)
+    G.compare_full(inp, out, lse, kv)
