@@ -69,11 +69,17 @@ __device__ __forceinline__ bool timed_wait(Ctrl* c, uint64_t* bar, uint32_t pari
   return false;
 }
 
+// For all lanes of a warp that goes on to collective instructions: either all of
+// them go on or, if the limit ran out for one, none.
+__device__ __forceinline__ bool timed_wait_all(Ctrl* c, uint64_t* bar, uint32_t parity, const DecodeParams& p) {
+  return __all_sync(0xffffffffu, timed_wait(c, bar, parity, p)) != 0;
+}
+
 // Barrier among the softmax threads, built on an mbarrier so the wait is
 // bounded (a named barrier would hang if a member gave up).
 __device__ __forceinline__ bool group_sync(Ctrl* c, uint64_t* bar, uint32_t& phase, const DecodeParams& p) {
   mbar_arrive(bar);
-  const bool ok = timed_wait(c, bar, phase & 1, p);
+  const bool ok = timed_wait_all(c, bar, phase & 1, p);
   ++phase;
   return ok;
 }
@@ -295,7 +301,7 @@ __global__ void __launch_bounds__(fp4::kThreads, 1)
         uint4 vmask;
         if (SPARSE) {
           const int d = gt % fp4::kRowDepth;
-          if (!timed_wait(c, &rt->full[d], (gt / fp4::kRowDepth) & 1, p)) { stop = true; break; }
+          if (!timed_wait_all(c, &rt->full[d], (gt / fp4::kRowDepth) & 1, p)) { stop = true; break; }
           vmask = *reinterpret_cast<const uint4*>(rt->valid[d]);
           __syncwarp();
           if (lane == 0) mbar_arrive(&rt->empty[d]);
@@ -307,7 +313,7 @@ __global__ void __launch_bounds__(fp4::kThreads, 1)
           };
           vmask = make_uint4(word(0), word(1), word(2), word(3));
         }
-        if (!timed_wait(c, &c->s_full[b], (gt >> 1) & 1, p)) { stop = true; break; }
+        if (!timed_wait_all(c, &c->s_full[b], (gt >> 1) & 1, p)) { stop = true; break; }
         tc_fence_after();
         if (k == pc.t0) scale_log2 = fp4::row_scale(p.scale_log2, c->q_back[pi & 1][r & 63]);
         const uint32_t s_addr = tmem + lane_base + kTmemS + 128 * b;
@@ -355,7 +361,7 @@ __global__ void __launch_bounds__(fp4::kThreads, 1)
         const bool do_rescale = *(volatile int*)&c->rescale_flag[gt & 1] != 0;
         // the O MMAs of the previous tile must be complete before O^T is
         // rescaled and before P^T (which they read) is overwritten
-        if (gt >= 1 && !timed_wait(c, &c->o_done, (gt - 1) & 1, p)) { stop = true; break; }
+        if (gt >= 1 && !timed_wait_all(c, &c->o_done, (gt - 1) & 1, p)) { stop = true; break; }
         tc_fence_after();
         if (do_rescale) {
 #pragma unroll 1
@@ -398,7 +404,7 @@ __global__ void __launch_bounds__(fp4::kThreads, 1)
       }
       if (stop) break;
       // ---------------- epilogue of the piece
-      if (last_gt >= 0 && !timed_wait(c, &c->o_done, last_gt & 1, p)) { stop = true; break; }
+      if (last_gt >= 0 && !timed_wait_all(c, &c->o_done, last_gt & 1, p)) { stop = true; break; }
       tc_fence_after();
       if (owner) {
         float inv = 0.f, lse = -INFINITY;

@@ -92,9 +92,15 @@ __device__ __forceinline__ bool pwait(const Pair& pr, uint64_t* bar, uint32_t pa
   return false;
 }
 
+// For all lanes of a warp that goes on to collective instructions: either all of
+// them go on or, if the limit ran out for one, none.
+__device__ __forceinline__ bool pwait_all(const Pair& pr, uint64_t* bar, uint32_t parity, const DecodeParams& p) {
+  return __all_sync(0xffffffffu, pwait(pr, bar, parity, p)) != 0;
+}
+
 __device__ __forceinline__ bool group_sync(const Pair& pr, uint32_t& phase, const DecodeParams& p) {
   mbar_arrive(&pr.c->grp_sm);
-  const bool ok = pwait(pr, &pr.c->grp_sm, phase & 1, p);
+  const bool ok = pwait_all(pr, &pr.c->grp_sm, phase & 1, p);
   ++phase;
   return ok;
 }
@@ -313,7 +319,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
         uint4 vm;
         if (SPARSE) {
           const int d = gt % fp4::kRowDepth;
-          if (!pwait(pr, &rt->full[d], (gt / fp4::kRowDepth) & 1, p)) { stop = true; break; }
+          if (!pwait_all(pr, &rt->full[d], (gt / fp4::kRowDepth) & 1, p)) { stop = true; break; }
           vm = rvalid ? *reinterpret_cast<const uint4*>(&rt->valid[d][4 * half]) : make_uint4(0, 0, 0, 0);
           __syncwarp();
           if (lane == 0) mbar_arrive(&rt->empty[d]);
@@ -326,7 +332,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
           };
           vm = make_uint4(word(0), word(1), word(2), word(3));
         }
-        if (!pwait(pr, &c->s_full[b], (gt >> 1) & 1, p)) { stop = true; break; }
+        if (!pwait_all(pr, &c->s_full[b], (gt >> 1) & 1, p)) { stop = true; break; }
         tc_fence_after();
         if (k == pc.t0) scale_log2 = fp4::row_scale(p.scale_log2, c->q_back[pi & 1][row]);
         const uint32_t s_addr = tmem + lane_base + kTmemS + 128 * b;
@@ -381,7 +387,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
         };
         uint32_t pk[16];
         probs(0, pk);
-        if (gt >= 1 && !pwait(pr, &c->o_done[(gt - 1) & 1], ((gt - 1) >> 1) & 1, p)) { stop = true; break; }
+        if (gt >= 1 && !pwait_all(pr, &c->o_done[(gt - 1) & 1], ((gt - 1) >> 1) & 1, p)) { stop = true; break; }
         store(0, pk);
 #pragma unroll 1
         for (int w = 1; w < 4; ++w) {
@@ -419,7 +425,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
       c->lx[half][row] = l_sum;
       if (!group_sync(pr, gph, p)) { stop = true; break; }
       const float l_tot = l_sum + c->lx[half ^ 1][row];
-      if (last_gt >= 0 && !pwait(pr, &c->o_done[last_gt & 1], (last_gt >> 1) & 1, p)) { stop = true; break; }
+      if (last_gt >= 0 && !pwait_all(pr, &c->o_done[last_gt & 1], (last_gt >> 1) & 1, p)) { stop = true; break; }
       tc_fence_after();
       float inv = 0.f, lse = -INFINITY;
       if (l_tot > 0.f) {

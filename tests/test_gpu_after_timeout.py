@@ -47,3 +47,29 @@ def test_shortest_limit(kv, h_q):
     out, lse, r = G.run_gpu(inp, dict(timeout_ns=1))
     assert r.status() == (M.MLA_OK, 0)
     G.compare_full(inp, out, lse, kv)
+
+
+@pytest.mark.parametrize("kv,h_q", [("fp4", 16), ("fp4", 128)])
+def test_limits_that_run_out_anywhere(kv, h_q):
+    """Units of 2 to 8 ms on few parts under limits of 1 to 8 ms: the wait for the
+    next unit's query, and with it every other role's, runs out at some point of
+    the work. The call returns, says so, and the next decode is right."""
+    w = dataclasses.replace(W.get_workload("tiny"), batch=3, s_q=1, h_q=h_q, seqlens=[120000, 40000, 33333], causal=False, kv=kv, seed=229)
+    d = G.to_device(W.make_inputs(w))
+    make = lambda **kw: M.DecodeRunner(d["q"], d["kcache"], d["block_table"], d["cache_seqlens"], softmax_scale=w.scale,  # noqa: E731
+                                       num_sm_parts=2, **kw)
+    good = make()
+    good.plan()
+    want = [t.clone() for t in good.run()]
+    gave_up = 0
+    for ms in (1.0, 1.3, 1.7, 2.2, 2.9, 3.7, 4.8, 6.2, 8.0):
+        r = make(timeout_ns=int(ms * 1e6))
+        r.plan()
+        r.run()
+        code, bits = r.status()
+        assert (code, bits) in ((M.MLA_OK, 0), (M.MLA_ERR_DEVICE_TIMEOUT, M.MLA_DEVICE_STATUS_TIMEOUT))
+        gave_up += code != M.MLA_OK
+        out, lse = good.run()
+        assert good.status() == (M.MLA_OK, 0)
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    assert gave_up > 0
