@@ -91,11 +91,18 @@ __device__ __forceinline__ bool timed_wait(Ctrl* c, uint64_t* bar, uint32_t pari
   return false;
 }
 
+// For all lanes of a warp that goes on to collective instructions: either all of
+// them go on or, if the limit ran out for one, none.
+__device__ __forceinline__ bool timed_wait_all(Ctrl* c, uint64_t* bar, uint32_t parity, const DecodeParams& p) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, timed_wait(c, bar, parity, p)) != 0;
+}
+
 // Barrier among the threads of one warp group, built on an mbarrier so the
 // wait is bounded (a named barrier would hang if a member gave up).
 __device__ __forceinline__ bool group_sync(Ctrl* c, uint64_t* bar, uint32_t& phase, const DecodeParams& p) {
   mbar_arrive(bar);
-  const bool ok = timed_wait(c, bar, phase & 1, p);
+  const bool ok = timed_wait_all(c, bar, phase & 1, p);
   ++phase;
   return ok;
 }
@@ -226,7 +233,7 @@ __device__ void gather_group(const DecodeParams& p, Ctrl* c, PieceIter& it, cons
       for (int j = 0; j < slots_per_tile; ++j, ++seq) {
         const int slot = seq % g.nslots;
         uint8_t* s = g.base + slot * kSlot;
-        if (!timed_wait(c, &g.empty[slot], ((seq / g.nslots) & 1) ^ 1, p)) { stop = true; break; }
+        if (!timed_wait_all(c, &g.empty[slot], ((seq / g.nslots) & 1) ^ 1, p)) { stop = true; break; }
         if (KGROUP) {
           if (MODE == kModeSparse || j == 8) {  // bf16 128-B row slice: 8 lanes per row
             const int off = MODE == kModeSparse ? 128 * j : 528;
@@ -548,7 +555,7 @@ __global__ void __launch_bounds__(MODE == kModeBf16 ? 256 : 256 + 2 * kGatherThr
           };
           vmask = make_uint4(word(0), word(1), word(2), word(3));
         }
-        if (!timed_wait(c, &c->s_full[b], (gt >> 1) & 1, p)) { stop = true; break; }
+        if (!timed_wait_all(c, &c->s_full[b], (gt >> 1) & 1, p)) { stop = true; break; }
         tc_fence_after();
         const uint32_t s_addr = tmem + lane_base + kTmemS + 128 * b;
         // pass 1: tile max
@@ -603,7 +610,7 @@ __global__ void __launch_bounds__(MODE == kModeBf16 ? 256 : 256 + 2 * kGatherThr
         const bool do_rescale = *(volatile int*)&c->rescale_flag[gt & 1] != 0;
         // the O MMAs of the previous tile must be complete before O^T is
         // rescaled and before P^T (which they read) is overwritten
-        if (gt >= 1 && !timed_wait(c, &c->o_done, (gt - 1) & 1, p)) { stop = true; break; }
+        if (gt >= 1 && !timed_wait_all(c, &c->o_done, (gt - 1) & 1, p)) { stop = true; break; }
         tc_fence_after();
         if (do_rescale) {
 #pragma unroll 1
@@ -648,7 +655,7 @@ __global__ void __launch_bounds__(MODE == kModeBf16 ? 256 : 256 + 2 * kGatherThr
       }
       if (stop) break;
       // ---------------- epilogue of the piece
-      if (last_gt >= 0 && !timed_wait(c, &c->o_done, last_gt & 1, p)) { stop = true; break; }
+      if (last_gt >= 0 && !timed_wait_all(c, &c->o_done, last_gt & 1, p)) { stop = true; break; }
       tc_fence_after();
       if (owner) {
         float inv = 0.f, lse = -INFINITY;

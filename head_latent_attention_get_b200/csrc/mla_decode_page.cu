@@ -90,10 +90,17 @@ __device__ __forceinline__ bool timed_wait(Ctrl* c, uint64_t* bar, uint32_t pari
   return false;
 }
 
+// For all lanes of a warp that goes on to collective instructions: either all of
+// them go on or, if the limit ran out for one, none.
+__device__ __forceinline__ bool timed_wait_all(Ctrl* c, uint64_t* bar, uint32_t parity, const DecodeParams& p) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, timed_wait(c, bar, parity, p)) != 0;
+}
+
 // Bounded barrier of a thread group, built on an mbarrier.
 __device__ __forceinline__ bool group_sync(Ctrl* c, uint64_t* bar, uint32_t& phase, const DecodeParams& p) {
   mbar_arrive(bar);
-  const bool ok = timed_wait(c, bar, phase & 1, p);
+  const bool ok = timed_wait_all(c, bar, phase & 1, p);
   ++phase;
   return ok;
 }
@@ -242,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int pj = 2 * pc.t0; pj < pend; ++pj, ++gp) {
         const int slot = gp & 1;
         uint8_t* s = sS + slot * kSlotB;
-        if (!timed_wait(c, &c->raw_full[slot], (gp >> 1) & 1, p)) { stop = true; break; }
+        if (!timed_wait_all(c, &c->raw_full[slot], (gp >> 1) & 1, p)) { stop = true; break; }
         // every converter reads its raw bytes before any slice row
         // overwrites them (the slices overlap the raw area)
         const bool live = kPage * pj + tk < Ls;  // rows past the request's end are written as zeros
@@ -260,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const unsigned long long sc8 = ((unsigned long long)scw.y << 32) | scw.x;
           __syncwarp();
           if (lane == 0) mbar_arrive(&c->grp_cv);
-          if (!timed_wait(c, &c->grp_cv, cph & 1, p)) { stop = true; break; }
+          if (!timed_wait_all(c, &c->grp_cv, cph & 1, p)) { stop = true; break; }
           ++cph;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -288,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           rope[1] = *reinterpret_cast<const uint4*>(rec + 528 + 32 * qq + 16);
           __syncwarp();
           if (lane == 0) mbar_arrive(&c->grp_cv);
-          if (!timed_wait(c, &c->grp_cv, cph & 1, p)) { stop = true; break; }
+          if (!timed_wait_all(c, &c->grp_cv, cph & 1, p)) { stop = true; break; }
           ++cph;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
@@ -406,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int nv = max(0, min(kPage, limit - kPage * pj));
         const uint32_t vw0 = nv >= 32 ? 0xffffffffu : ((1u << max(nv, 0)) - 1u);
         const uint32_t vw1 = nv >= 64 ? 0xffffffffu : (nv <= 32 ? 0u : ((1u << (nv - 32)) - 1u));
-        if (!timed_wait(c, &c->s_full[b], (gp >> 1) & 1, p)) { stop = true; break; }
+        if (!timed_wait_all(c, &c->s_full[b], (gp >> 1) & 1, p)) { stop = true; break; }
         tc_fence_after();
         const uint32_t s_addr = tmem + lane_base + kTmemS + 64 * b;
         // pass 1: page max
@@ -461,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool do_rescale = *(volatile int*)&c->rescale_flag[gp & 1] != 0;
         // the O MMAs of the previous page must be complete before O^T is
         // rescaled and before P^T (which they read) is overwritten
-        if (gp >= 1 && !timed_wait(c, &c->o_done, (gp - 1) & 1, p)) { stop = true; break; }
+        if (gp >= 1 && !timed_wait_all(c, &c->o_done, (gp - 1) & 1, p)) { stop = true; break; }
         tc_fence_after();
         if (do_rescale) {
 #pragma unroll 1
@@ -506,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (stop) break;
       // ---------------- epilogue of the piece
-      if (last_gp >= 0 && !timed_wait(c, &c->o_done, last_gp & 1, p)) { stop = true; break; }
+      if (last_gp >= 0 && !timed_wait_all(c, &c->o_done, last_gp & 1, p)) { stop = true; break; }
       tc_fence_after();
       if (owner) {
         float inv = 0.f, lse = -INFINITY;

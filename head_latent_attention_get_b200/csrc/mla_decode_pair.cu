@@ -117,9 +117,15 @@ __device__ __forceinline__ bool pwait(const Pair& pr, uint64_t* bar, uint32_t pa
   return false;
 }
 
+// For all lanes of a warp that goes on to collective instructions: either all of
+// them go on or, if the limit ran out for one, none.
+__device__ __forceinline__ bool pwait_all(const Pair& pr, uint64_t* bar, uint32_t parity, const DecodeParams& p) {
+  return __all_sync(0xffffffffu, pwait(pr, bar, parity, p)) != 0;
+}
+
 __device__ __forceinline__ bool group_sync(const Pair& pr, uint32_t& phase, const DecodeParams& p) {
   mbar_arrive(&pr.c->grp_sm);
-  const bool ok = pwait(pr, &pr.c->grp_sm, phase & 1, p);
+  const bool ok = pwait_all(pr, &pr.c->grp_sm, phase & 1, p);
   ++phase;
   return ok;
 }
@@ -539,7 +545,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SPARSE ? kThreadsSpa
         // validity of this thread's 128 keys: bit i of word w = key 32w + i
         uint4 vm;
         if (SPARSE) {
-          if (!pwait(pr, &c->m_full[gt & 3], (gt >> 2) & 1, p)) { stop = true; break; }
+          if (!pwait_all(pr, &c->m_full[gt & 3], (gt >> 2) & 1, p)) { stop = true; break; }
           vm = rvalid ? *reinterpret_cast<const uint4*>(&c->vmask[gt & 3][4 * half]) : make_uint4(0, 0, 0, 0);
         } else {
           const int tile = k + half;
@@ -550,7 +556,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SPARSE ? kThreadsSpa
           };
           vm = make_uint4(word(0), word(1), word(2), word(3));
         }
-        if (!pwait(pr, &c->s_full[b], (gt >> 1) & 1, p)) { stop = true; break; }
+        if (!pwait_all(pr, &c->s_full[b], (gt >> 1) & 1, p)) { stop = true; break; }
         tc_fence_after();
         const uint32_t s_addr = tmem + lane_base + kTmemS + 128 * b;
         // pass 1: max over this thread's 128 keys
@@ -614,7 +620,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SPARSE ? kThreadsSpa
           uint32_t pk[2][16];
 #pragma unroll
           for (int w = 0; w < 2; ++w) probs(w, pk[w]);
-          if (gt >= 1 && !pwait(pr, &c->o_done[(gt - 1) & 1], ((gt - 1) >> 1) & 1, p)) { stop = true; break; }
+          if (gt >= 1 && !pwait_all(pr, &c->o_done[(gt - 1) & 1], ((gt - 1) >> 1) & 1, p)) { stop = true; break; }
 #pragma unroll
           for (int w = 0; w < 2; ++w) store(w, pk[w]);
 #pragma unroll 1
@@ -652,7 +658,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SPARSE ? kThreadsSpa
       c->lx[half][row] = l_sum;
       if (!group_sync(pr, gph, p)) { stop = true; break; }
       const float l_tot = l_sum + c->lx[half ^ 1][row];
-      if (last_gt >= 0 && !pwait(pr, &c->o_done[last_gt & 1], (last_gt >> 1) & 1, p)) { stop = true; break; }
+      if (last_gt >= 0 && !pwait_all(pr, &c->o_done[last_gt & 1], (last_gt >> 1) & 1, p)) { stop = true; break; }
       tc_fence_after();
       float inv = 0.f, lse = -INFINITY;
       if (l_tot > 0.f) {

@@ -17,8 +17,18 @@ pytestmark = pytest.mark.gpu
 def test_decodes_after_timeouts(h_q, topk):
     """Scores withheld: the loaders stop with copies in flight, for every part
     of the grid at once. A good decode follows in the same stream each time."""
+    check_after_timeouts("fp4", h_q, topk)
+
+
+@pytest.mark.parametrize("kv,h_q,topk", [("bf16", 16, 0), ("bf16", 16, 1024), ("bf16", 128, 0), ("bf16", 128, 1024), ("fp8", 64, 0),
+                                         ("fp8", 64, 1024)])
+def test_decodes_after_timeouts_other_caches(kv, h_q, topk):
+    check_after_timeouts(kv, h_q, topk)
+
+
+def check_after_timeouts(kv, h_q, topk):
     w = dataclasses.replace(W.get_workload("tiny"), batch=40, s_q=1, h_q=h_q, seqlens=[1500 + 37 * i for i in range(40)], causal=False,
-                            topk=topk, kv="fp4", seed=211)
+                            topk=topk, kv=kv, seed=211)
     d = G.to_device(W.make_inputs(w, poison_tail=True))
     make = lambda **kw: M.DecodeRunner(d["q"], d["kcache"], d["block_table"], d["cache_seqlens"], softmax_scale=w.scale,  # noqa: E731
                                        indices=d["indices"], **kw)
@@ -55,14 +65,18 @@ def test_limits_that_run_out_anywhere(kv, h_q):
     next unit's query, and with it every other role's, runs out at some point of
     the work. The call returns, says so, and the next decode is right."""
     w = dataclasses.replace(W.get_workload("tiny"), batch=3, s_q=1, h_q=h_q, seqlens=[120000, 40000, 33333], causal=False, kv=kv, seed=229)
+    check_limits(w, 2, (1.0, 1.3, 1.7, 2.2, 2.9, 3.7, 4.8, 6.2, 8.0))
+
+
+def check_limits(w, parts, limits):
     d = G.to_device(W.make_inputs(w))
     make = lambda **kw: M.DecodeRunner(d["q"], d["kcache"], d["block_table"], d["cache_seqlens"], softmax_scale=w.scale,  # noqa: E731
-                                       num_sm_parts=2, **kw)
+                                       num_sm_parts=parts, **kw)
     good = make()
     good.plan()
     want = [t.clone() for t in good.run()]
     gave_up = 0
-    for ms in (1.0, 1.3, 1.7, 2.2, 2.9, 3.7, 4.8, 6.2, 8.0):
+    for ms in limits:
         r = make(timeout_ns=int(ms * 1e6))
         r.plan()
         r.run()
