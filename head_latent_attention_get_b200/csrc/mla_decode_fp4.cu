@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(fp4::kThreads, 1)
         float inv = 0.f, lse = -INFINITY;
         if (l_sum > 0.f) {
           inv = 1.f / l_sum;
-          lse = m_used * scale_log2 * 0.693147181f + logf(l_sum);
+          lse = m_used * scale_log2 * 0.693147181f + logf(l_sum * fp4::kProbInv);
         }
         if (pc.single && rvalid && p.sink != nullptr) inv *= fold_sink(lse, p.sink[row_head(p, pc.unit, row0 + r)]);
         c->inv_l[r] = inv;

@@ -430,7 +430,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
       float inv = 0.f, lse = -INFINITY;
       if (l_tot > 0.f) {
         inv = 1.f / l_tot;
-        lse = m_used * scale_log2 * 0.693147181f + logf(l_tot);
+        lse = m_used * scale_log2 * 0.693147181f + logf(l_tot * fp4::kProbInv);
       }
       if (pc.single && rvalid && p.sink != nullptr) inv *= fold_sink(lse, p.sink[row_head(p, pc.unit, grow)]);
       const size_t orow = (size_t)pc.unit * p.rows + grow;

@@ -186,17 +186,23 @@ __device__ __forceinline__ void mask_scores(uint32_t (&sv)[32], uint32_t valid) 
     if (!((valid >> i) & 1u)) sv[i] = 0xff800000u;
 }
 
-// Probabilities of 32 keys from their scores: 2^((s - m) * scale_log2), as f16
-// pairs, and their sums added to `sum` (even and odd keys). The difference is
+// Probabilities of 32 keys from their scores: 2^((s - m) * scale_log2 + 7), as
+// f16 pairs, and their sums added to `sum` (even and odd keys). The difference is
 // taken first: a product rounded before it would be off by more than 1 for
 // scores past 2^24. A masked score is -inf: e^-inf = 0.
+// The 7: the largest is then 2^7 and, before O is rescaled, 2^15 of f16's 65504 at
+// most, and those down to 2^-21 of the largest keep f16's 11 bits, down to 2^-31
+// some. Without it 2^-25 was 0 in the product with V but not in the sum, up to
+// 2^-8 of the output at 128K keys. The sum has the same factor, so that it cancels
+// in the output; the log-sum-exp takes it out. Times are the same.
+constexpr float kProbLog2 = 7.0f, kProbInv = 0.0078125f;
 __device__ __forceinline__ void probabilities(const uint32_t (&sv)[32], float m, float scale_log2, uint32_t (&pk)[16],
                                               uint64_t& sum) {
-  const uint64_t nm = join2(-m, -m), sl = join2(scale_log2, scale_log2);
+  const uint64_t nm = join2(-m, -m), sl = join2(scale_log2, scale_log2), up = join2(kProbLog2, kProbLog2);
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     float x0, x1;
-    split2(mul2(add2(join2(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1])), nm), sl), x0, x1);
+    split2(fma2(add2(join2(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1])), nm), sl, up), x0, x1);
     x0 = ex2_approx(x0);
     x1 = ex2_approx(x1);
     pk[i] = pack_f16x2(x0, x1);
