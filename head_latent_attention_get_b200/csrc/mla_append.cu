@@ -219,6 +219,24 @@ extern "C" mla_status_t mla_kv_append(const void* kv, long long kv_stride, int t
   if (gamma && !(eps >= 0.f)) return MLA_ERR_INVALID_ARG;
   if (nvfp4 && (!kv_scale || !al16(kv_scale))) return MLA_ERR_INVALID_ARG;
   if ((long long)num_pages * kPage > 0x7fffffffLL || tokens > (1 << 30)) return MLA_ERR_UNSUPPORTED;
+  const size_t T = (size_t)tokens, rows = (size_t)num_pages * kPage;
+  const size_t row_bytes = kv_format == MLA_KV_BF16       ? kDqk * 2
+                           : kv_format == MLA_KV_FP8_E4M3 ? kFp8RecordBytes
+                           : nvfp4                        ? kNvfp4RowBytes
+                                                          : kFp4RecordBytes;
+  const size_t angles = rope_cos ? T * (kRope / 2) * 4 : 0;
+  const struct { const void* p; size_t n; } in[] = {{kv, ((T - 1) * (size_t)kv_stride + d_qk) * 2}, {gamma, gamma ? kDv * 4 : 0},
+                                                    {rope_cos, angles}, {rope_sin, angles}, {slots, T * 4}};
+  const struct { const void* p; size_t n; } out[] = {{kcache, rows * row_bytes}, {kv_scale, nvfp4 ? rows * kNvfp4ScaleBytes : 0},
+                                                     {kv_out, kv_out ? T * d_qk * 2 : 0}, {status, status ? sizeof(*status) : 0}};
+  for (int i = 0; i < 4; ++i) {
+    for (int j = 0; j < 5; ++j)
+      // rows are read whole before they are written: kv_out may be kv itself
+      if (overlap(out[i].p, out[i].n, in[j].p, in[j].n) && !(i == 2 && j == 0 && kv_out == kv && kv_stride == d_qk))
+        return MLA_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i].p, out[i].n, out[j].p, out[j].n)) return MLA_ERR_INVALID_ARG;
+  }
   const AppendParams p{static_cast<const __nv_bfloat16*>(kv), gamma, rope_cos, rope_sin, slots,
                        static_cast<uint8_t*>(kcache), static_cast<uint8_t*>(kv_scale),
                        static_cast<__nv_bfloat16*>(kv_out), status, kv_stride, tokens, num_pages * kPage, eps};

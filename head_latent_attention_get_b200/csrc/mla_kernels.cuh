@@ -109,4 +109,10 @@ mla_status_t launch_metadata(const int32_t* seqlens, int U, int upr, int topk, i
 mla_status_t launch_combine(const void* workspace, int units, int rows, int parts, const int32_t* split_ptr,
                             int h_q, const float* sink, void* out, float* lse, cudaStream_t stream);
 
+// Host side: do two buffers of na and nb bytes share one?
+inline bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return na && nb && x < y + nb && y < x + na;
+}
+
 }  // namespace mla

@@ -400,10 +400,11 @@ mla_status_t mla_extend_tables(const int32_t* context_lens, const int32_t* new_l
  *   kv_out    device bf16 [tokens][d_qk] or NULL: the values that the cache now
  *             holds (what decoding reads), for attention over the new tokens;
  *             rows without a slot are left alone. It may be kv when
- *             kv_stride == d_qk.
+ *             kv_stride == d_qk; otherwise the outputs (kcache, kv_scale,
+ *             kv_out, status) overlap neither the inputs nor each other.
  * kv, kcache, kv_scale, kv_out and gamma 16-byte aligned, kv_stride a multiple
- * of 8. Errors: INVALID_ARG (null or misaligned pointers, a bad format, d_qk,
- * stride or size, one of rope_cos / rope_sin without the other, eps < 0),
+ * of 8. Errors: INVALID_ARG (null, misaligned or overlapping buffers, a bad
+ * format, d_qk, stride or size, one of rope_cos / rope_sin without the other, eps < 0),
  * UNSUPPORTED (num_pages * 64 above 2^31 - 1, tokens above 2^30), CUDA. */
 mla_status_t mla_kv_append(const void* kv, long long kv_stride, int tokens, int d_qk, const float* gamma, float eps,
                            const float* rope_cos, const float* rope_sin, const int32_t* slots, void* kcache,
