@@ -394,7 +394,12 @@ mla_status_t mla_extend_tables(const int32_t* context_lens, const int32_t* new_l
  *     slot: its record could then hold parts of both.
  * The factor 1 / sqrt(..) is rounded to fp32 from 64-bit arithmetic and every
  * fp32 product, sum and quotient once, so the stored bytes are a function of
- * the inputs. NaN inputs give unspecified codes in their row.
+ * the inputs. Values that are not finite: BF16 stores them; an infinity gives
+ * its FP8 tile an infinite scale, so that its 128 values decode to NaN, and is
+ * saturated by E2M1 (scale 448, code +-6; its block's other values as for any
+ * maximum above 2688); a NaN gives unspecified codes in its tile or block. The
+ * norm (gamma given) carries either into the whole row, and makes a row of
+ * zeros NaN when eps is 0. Other tiles, blocks and rows are as without it.
  *   kcache    device, format per kv_format (MLA_KV_*), 16-byte aligned;
  *   kv_scale  MLA_KV_NVFP4: device uint8 [num_pages, 64, 32], else ignored;
  *   kv_out    device bf16 [tokens][d_qk] or NULL: the values that the cache now
