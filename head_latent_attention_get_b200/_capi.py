@@ -118,18 +118,27 @@ def _ptr(t):
     return t.data_ptr()
 
 
-_raw_stream = None
+_device_calls = None
+
+
+def _device():
+    """(current device, raw current stream of a device) as two functions. Building
+    a torch.cuda.Stream costs more than a small kernel (3 us), so torch's internal
+    calls for both are used where this version has them, else the public ones."""
+    global _device_calls
+    if _device_calls is None:
+        import torch
+        torch.cuda.current_stream()  # initialises CUDA
+        _device_calls = (getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device,
+                         getattr(torch._C, "_cuda_getCurrentRawStream", None)
+                         or (lambda device: torch.cuda.current_stream(device).cuda_stream))
+    return _device_calls
 
 
 def _stream(stream):
     if stream is None:
-        # the raw handle: building a torch.cuda.Stream costs more than a small kernel
-        global _raw_stream
-        if _raw_stream is None:
-            import torch
-            torch.cuda.current_stream()  # initialises CUDA
-            _raw_stream = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
-        return _raw_stream[0](_raw_stream[1]())
+        device, raw_stream = _device()
+        return raw_stream(device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
