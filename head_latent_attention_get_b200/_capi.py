@@ -40,8 +40,8 @@ FP4_RECORD_BYTES = 416  # bytes of one MLA_KV_FP4_E2M1 token record
 
 
 class MLAError(RuntimeError):
-    def __init__(self, code: int, where: str):
-        super().__init__(f"{where}: {mla_status_string(code)} ({code})")
+    def __init__(self, code: int, where: str, why: str = ""):
+        super().__init__(f"{where}: {mla_status_string(code)} ({code}){': ' if why else ''}{why}")
         self.code = code
 
 
@@ -258,19 +258,87 @@ def mla_out_rope_fp8(out, batch, s_q, h_q, d_qk, rope_cos, rope_sin, out_fp8, ou
                                   _ptr(out_fp8), _ptr(out_scale), _stream(stream)), "mla_out_rope_fp8")
 
 
+def _pointers(where, device, tensors):
+    """Data pointers of (name, tensor or None, element types, bytes, dense), None for
+    None. Refuses what the library would misread or read out of bounds: a tensor
+    must be on `device`, the current one, of one of the element types (the usual one
+    first), without gaps (or, not dense, without gaps in its last dimension), and
+    have `bytes` of memory from its first element on."""
+    out = []
+    for name, t, types, need, dense in tensors:
+        if t is None:
+            out.append(None)
+            continue
+        try:
+            if t.dtype is types[0] and t.get_device() == device and t.is_contiguous() and t.nbytes >= need:
+                out.append(t.data_ptr())
+                continue
+            at = t.get_device()
+        except AttributeError:
+            at = -1
+        if at != device:
+            why = f"must be on the current CUDA device ({device})" + (f", not on {at}" if at >= 0 else "")
+        elif t.dtype not in types:
+            why = f"must be {' or '.join(map(str, types))}, not {t.dtype}"
+        elif not (t.is_contiguous() if dense else t.dim() == 0 or t.stride(-1) == 1):
+            why = f"must be contiguous{'' if dense else ' in its last dimension'}"
+        elif t.untyped_storage().nbytes() - t.storage_offset() * t.element_size() < need or (dense and t.nbytes < need):
+            why = f"is too small: {need} bytes are used"
+        else:
+            out.append(t.data_ptr())
+            continue
+        raise MLAError(MLA_ERR_INVALID_ARG, where, f"{name} {why}")
+    return out
+
+
+_types = None
+
+
+def _element_types():
+    """(int32, float32, bf16, status words, per kv_format: bytes of a token in kcache and
+    its types, of NVFP4 scales). A status word may be the first of a decode workspace."""
+    global _types
+    if _types is None:
+        from torch import bfloat16, float32, float8_e4m3fn, int32, uint8, uint32
+        u8 = (uint8,)
+        _types = ((int32,), (float32,), (bfloat16,), (int32, uint32, uint8),
+                  {MLA_KV_BF16: (1152, (bfloat16, uint8)), MLA_KV_FP8_E4M3: (656, u8), MLA_KV_NVFP4: (256, u8),
+                   MLA_KV_FP4_E2M1: (FP4_RECORD_BYTES, u8)}, (uint8, float8_e4m3fn))
+    return _types
+
+
 def mla_extend_tables(context_lens, new_lens, batch, free_pages, free_range, num_pages, block_table,
                       block_table_stride, seqlens, token_start, slots, positions, max_tokens, free_next, status=None,
                       stream=None):
     """num_free is the length of free_pages (a tensor, or None for an empty list)."""
+    device, raw_stream = _device()
+    device = device()
+    i32, _, _, word, _, _ = _element_types()
+    row = 4 * batch
+    p = _pointers("mla_extend_tables", device, (
+        ("context_lens", context_lens, i32, row, True), ("new_lens", new_lens, i32, row, True),
+        ("free_pages", free_pages, i32, 0, True), ("free_range", free_range, i32, 8, True),
+        ("block_table", block_table, i32, row * block_table_stride, False), ("seqlens", seqlens, i32, row, True),
+        ("token_start", token_start, i32, row + 4, True), ("slots", slots, i32, 4 * max_tokens, True),
+        ("positions", positions, i32, 4 * max_tokens, True), ("free_next", free_next, i32, 4, True), ("status", status, word, 4, True)))
     num_free = 0 if free_pages is None else free_pages.numel()
-    _check(lib().mla_extend_tables(_ptr(context_lens), _ptr(new_lens), batch, _ptr(free_pages), num_free,
-                                   _ptr(free_range), num_pages, _ptr(block_table), block_table_stride, _ptr(seqlens),
-                                   _ptr(token_start), _ptr(slots), _ptr(positions), max_tokens, _ptr(free_next),
-                                   _ptr(status), _stream(stream)), "mla_extend_tables")
+    _check(lib().mla_extend_tables(p[0], p[1], batch, p[2], num_free, p[3], num_pages, p[4], block_table_stride, p[5], p[6], p[7],
+                                   p[8], max_tokens, p[9], p[10], raw_stream(device) if stream is None else _stream(stream)),
+           "mla_extend_tables")
 
 
 def mla_kv_append(kv, kv_stride, tokens, d_qk, gamma, eps, rope_cos, rope_sin, slots, kcache, kv_scale, kv_format,
                   num_pages, kv_out=None, status=None, stream=None):
-    _check(lib().mla_kv_append(_ptr(kv), kv_stride, tokens, d_qk, _ptr(gamma), float(eps), _ptr(rope_cos),
-                               _ptr(rope_sin), _ptr(slots), _ptr(kcache), _ptr(kv_scale), kv_format, num_pages,
-                               _ptr(kv_out), _ptr(status), _stream(stream)), "mla_kv_append")
+    device, raw_stream = _device()
+    device = device()
+    i32, f32, bf16, word, records, scales = _element_types()
+    record, cache = records.get(kv_format, (0, scales))
+    angles = 128 * tokens
+    p = _pointers("mla_kv_append", device, (
+        ("kv", kv, bf16, 2 * ((tokens - 1) * kv_stride + d_qk), False), ("gamma", gamma, f32, 2048, True),
+        ("rope_cos", rope_cos, f32, angles, True), ("rope_sin", rope_sin, f32, angles, True), ("slots", slots, i32, 4 * tokens, True),
+        ("kcache", kcache, cache, num_pages * 64 * record, True),
+        ("kv_scale", kv_scale if kv_format == MLA_KV_NVFP4 else None, scales, num_pages * 64 * 32, True),
+        ("kv_out", kv_out, bf16, 2 * tokens * d_qk, True), ("status", status, word, 4, True)))
+    _check(lib().mla_kv_append(p[0], kv_stride, tokens, d_qk, p[1], float(eps), p[2], p[3], p[4], p[5], p[6], kv_format, num_pages,
+                               p[7], p[8], raw_stream(device) if stream is None else _stream(stream)), "mla_kv_append")
