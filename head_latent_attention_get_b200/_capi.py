@@ -36,7 +36,8 @@ MLA_DEBUG_SKIP_COMBINE = 2
 MLA_TILE_MD_INTS = 8
 MLA_MAX_ROWS = 128
 MLA_NOALLOC_WORKSPACE_BYTES = 48 << 20
-FP4_RECORD_BYTES = 416  # bytes of one MLA_KV_FP4_E2M1 token record
+FP8_RECORD_BYTES = 656  # bytes of one MLA_KV_FP8_E4M3 token record
+FP4_RECORD_BYTES = 416  # and of one MLA_KV_FP4_E2M1 token record
 
 
 class MLAError(RuntimeError):
@@ -302,7 +303,7 @@ def _element_types():
         from torch import bfloat16, float32, float8_e4m3fn, int32, uint8, uint32
         u8 = (uint8,)
         _types = ((int32,), (float32,), (bfloat16,), (int32, uint32, uint8),
-                  {MLA_KV_BF16: (1152, (bfloat16, uint8)), MLA_KV_FP8_E4M3: (656, u8), MLA_KV_NVFP4: (256, u8),
+                  {MLA_KV_BF16: (1152, (bfloat16, uint8)), MLA_KV_FP8_E4M3: (FP8_RECORD_BYTES, u8), MLA_KV_NVFP4: (256, u8),
                    MLA_KV_FP4_E2M1: (FP4_RECORD_BYTES, u8)}, (uint8, float8_e4m3fn))
     return _types
 

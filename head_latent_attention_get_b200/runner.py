@@ -32,7 +32,13 @@ class DecodeRunner:
             if kcache.dtype == torch.bfloat16:
                 self.kv_format = C.MLA_KV_BF16
             else:
-                self.kv_format = C.MLA_KV_FP4_E2M1 if kcache.shape[-1] == C.FP4_RECORD_BYTES else C.MLA_KV_FP8_E4M3
+                # the last dimension tells the format, and num_pages is taken from the
+                # first: both have to be what the cache's memory holds
+                formats = {C.FP8_RECORD_BYTES: C.MLA_KV_FP8_E4M3, C.FP4_RECORD_BYTES: C.MLA_KV_FP4_E2M1}
+                assert kcache.element_size() == 1 and kcache.shape[-1] in formats, "records are 656 (FP8) or 416 (4-bit) bytes"
+                assert kcache.is_contiguous() and kcache.numel() == kcache.shape[0] * 64 * kcache.shape[-1], \
+                    "a cache of records is [pages, 64, record bytes]"
+                self.kv_format = formats[kcache.shape[-1]]
             d_qk = 576
         self.q_scale, self.kv_scale = q_scale, kv_scale
         upr, self.rows = C.mla_decode_geometry(self.s_q, self.h_q, 1, self.topk)
