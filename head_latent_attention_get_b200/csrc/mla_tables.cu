@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(THREADS) extend_tables_kernel(const TableParam
       const int c = s_ctx[lo];
       int pos = -1, slot = -1;
       if (c >= 0) {
-        pos = c + t - s_start[lo];
+        pos = c + (t - s_start[lo]);  // c + t may pass 2^31
         const int j = pos / kPage;
         int pg;
         if ((long long)j * kPage >= c) {
