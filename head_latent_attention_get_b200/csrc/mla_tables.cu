@@ -259,17 +259,16 @@ extern "C" mla_status_t mla_extend_tables(const int32_t* context_lens, const int
   const struct { const void* p; size_t n; } out[] = {
       {block_table, (size_t)batch * block_table_stride * 4}, {seqlens, (size_t)batch * 4},
       {token_start, ((size_t)batch + 1) * 4}, {slots, (size_t)max_tokens * 4}, {positions, (size_t)max_tokens * 4},
-      {free_next, 4}};
+      {free_next, 4}, {status, status ? sizeof(*status) : 0}};
   for (int i = 0; i < 4; ++i)
     if ((!in[i].p && i < 3) || !aligned4(in[i].p)) return MLA_ERR_INVALID_ARG;
-  for (int i = 0; i < 6; ++i) {
-    if (!out[i].p || !aligned4(out[i].p)) return MLA_ERR_INVALID_ARG;
+  for (int i = 0; i < 7; ++i) {
+    if ((!out[i].p && i < 6) || !aligned4(out[i].p)) return MLA_ERR_INVALID_ARG;
     for (int j = 0; j < 4; ++j)
-      if (in[j].n && overlap(out[i].p, out[i].n, in[j].p, in[j].n)) return MLA_ERR_INVALID_ARG;
+      if (overlap(out[i].p, out[i].n, in[j].p, in[j].n)) return MLA_ERR_INVALID_ARG;
     for (int j = 0; j < i; ++j)
       if (overlap(out[i].p, out[i].n, out[j].p, out[j].n)) return MLA_ERR_INVALID_ARG;
   }
-  if (!aligned4(status)) return MLA_ERR_INVALID_ARG;
   if ((long long)num_pages * kPage > 0x7fffffffLL || (long long)block_table_stride * kPage > 0x7fffffffLL ||
       batch > (1 << 30) || max_tokens > (1 << 30))
     return MLA_ERR_UNSUPPORTED;

@@ -366,7 +366,7 @@ mla_status_t mla_out_rope_fp8(const void* out, int batch, int s_q, int h_q, int 
  *   slots, positions  device int32 [max_tokens], written
  *   free_next    device int32 [1], written: free_range[0] + pages taken, the
  *                next step's free_range[0]
- * The outputs must overlap neither the inputs nor each other. Errors:
+ * The outputs (status among them) must overlap neither the inputs nor each other. Errors:
  * INVALID_ARG (null, misaligned or overlapping buffers, non-positive sizes),
  * UNSUPPORTED (num_pages * 64 or block_table_stride * 64 above 2^31 - 1, batch
  * or max_tokens above 2^30), CUDA. */
