@@ -6,7 +6,10 @@
 //   bf16 = RNE(y), the rotated pairs RNE(x0 c - x1 s), RNE(x0 s + x1 c)
 //   FP8  per 128 values: scale = amax * (1 / 448) (1 if amax = 0), code = RNE(x / scale)
 //   FP4  per 16 values:  scale = e4m3(amax * (1 / 6)),             code = RNE(x / scale)
-// (1 / 448 and 1 / 6 rounded to fp32)
+// 1 / 448 and 1 / 6 are rounded to fp32. For E2M1 the product decides like the
+// quotient; an FP8 scale may differ from amax / 448 in its last bit (55 % of bf16
+// mantissas), and is the same as torch's amax / 448 on the GPU, which multiplies
+// by the reciprocal of a scalar: programs that fill a cache with torch get these bytes.
 //
 // A row map bound by HBM: 1152 bytes in, 416 out per token for 4-bit records.
 // One warp per token: lane l holds latent values 8l..8l+7 and 256+8l.. (an FP4

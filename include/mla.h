@@ -387,7 +387,10 @@ mla_status_t mla_extend_tables(const int32_t* context_lens, const int32_t* new_l
  *     cache's format: FP8 per 128 values with scale = amax * (1/448) (1 if amax
  *     is 0), the code of value / scale; E2M1 per 16 values with the UE4M3 scale
  *     of amax * (1/6), the code of value / scale (0 if the scale rounds to 0);
- *     1/448 and 1/6 rounded to fp32, codes to nearest even, saturating;
+ *     1/448 and 1/6 rounded to fp32, codes to nearest even, saturating (an FP8
+ *     scale is thus what torch's `amax / 448` gives on the GPU, where a scalar
+ *     divisor becomes a product, and may differ in its last bit from a divided
+ *     amax / 448 such as mla_out_rope_fp8's; the record is read by its own scale);
  *   - the row goes to cache slot slots[t] (page * 64 + token of the page).
  *     -1: the row is skipped; other values outside [0, num_pages * 64) are
  *     skipped and set MLA_DEVICE_STATUS_BOUNDS. Two rows must not name one
