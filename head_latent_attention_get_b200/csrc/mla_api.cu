@@ -115,8 +115,8 @@ mla_status_t run_decode(const mla_decode_args* a, const int32_t* indices, int to
   // and (bf16 paged cache only) the cache as [pages*64 tokens][576 dims];
   // boxes of 64 x 64 with 128-B swizzle. The FP8 and NVFP4 paged modes copy
   // whole pages with cp.async.bulk, the sparse modes gather rows with
-  // cp.async, 4-bit records are read by the converting threads: none of them
-  // needs a cache map.
+  // cp.async, 4-bit records are copied by loader warps: none of them needs a
+  // cache map.
   CUtensorMap tq, tkv, tv;
   std::memset(&tq, 0, sizeof(tq));
   std::memset(&tkv, 0, sizeof(tkv));

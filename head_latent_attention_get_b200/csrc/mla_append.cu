@@ -11,12 +11,14 @@
 // mantissas), and is the same as torch's amax / 448 on the GPU, which multiplies
 // by the reciprocal of a scalar: programs that fill a cache with torch get these bytes.
 //
-// A row map bound by HBM: 1152 bytes in, 416 out per token for 4-bit records.
-// One warp per token: lane l holds latent values 8l..8l+7 and 256+8l.. (an FP4
-// block is two lanes, an FP8 tile sixteen) and RoPE pair l, so every access of
-// the warp is contiguous. 32768 rows into 4-bit records, with the stored
-// values written too: 22.3 us, 4.4 TB/s or 0.67 of the measured copy; the norm's
-// 64-bit sum is 1 us of it, the rest is the scattered 416-byte records.
+// A row map, for 4-bit records 1152 bytes in and 416 out per token. One warp per
+// token: lane l holds latent values 8l..8l+7 and 256+8l.. (an FP4 block is two
+// lanes, an FP8 tile sixteen) and RoPE pair l, so every access of the warp is
+// contiguous. 32768 rows, without / with the stored values written too: 20 / 23 us
+// into 4-bit records, 21 / 23 FP8, 16 / 21 BF16 (floors at the measured copy rate
+// 9 / 15, 10 / 16, 13 / 19). Quantised rows are bound by instruction issue (4 bits:
+// 557 warp instructions a row, 3.1 a clock of 4; DRAM 26 %); the norm's 64-bit sum
+// is 1 us of it.
 // The codes are functions of the inputs alone, whatever the order of the sum:
 // the sum of squares is taken in 64 bits (squares of bf16 values; its rounding
 // reaches the fp32 factor about once in 2^29 rows), every fp32 operation after

@@ -223,7 +223,7 @@ typedef struct {
   int num_sm_parts;             /* the value passed to mla_get_metadata */
   float softmax_scale;          /* multiplies q.k before the softmax */
   int causal;                   /* nonzero: causal mask inside the s_q block */
-  int kv_format;                /* MLA_KV_BF16, MLA_KV_FP8_E4M3 or MLA_KV_NVFP4 */
+  int kv_format;                /* one of MLA_KV_* */
   uint64_t timeout_ns;          /* limit of every device wait; 0 = 2 s, below 1 ms counts as 1 ms */
   uint32_t debug_flags;         /* MLA_DEBUG_* test hooks; 0 normally */
   const float* sink;            /* device fp32 [h_q], 4-B aligned, or NULL: per-head
