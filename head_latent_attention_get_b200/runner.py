@@ -40,6 +40,22 @@ class DecodeRunner:
                     "a cache of records is [pages, 64, record bytes]"
                 self.kv_format = formats[kcache.shape[-1]]
             d_qk = 576
+        pages, requests = kcache.shape[0], self.batch
+        queries = requests * self.s_q * self.h_q
+        values = kcache.shape[-1] if kcache.element_size() == 1 else 576
+        for name, t, types, count in (
+                ("q", q, (torch.bfloat16, torch.uint8), queries * d), ("kcache", kcache, None, pages * 64 * values),
+                ("block_table", block_table, (torch.int32,), requests * block_table.shape[-1]),
+                ("cache_seqlens", cache_seqlens, (torch.int32,), requests),
+                ("indices", indices, (torch.int32,), requests * self.s_q * self.topk),
+                ("q_scale", q_scale, (torch.uint8, torch.float8_e4m3fn), queries * 32),
+                ("kv_scale", kv_scale, (torch.uint8, torch.float8_e4m3fn), pages * 64 * 32)):
+            # the kernels take pointers: what they would misread or fault on is refused here
+            if t is not None:
+                assert t.device == dev, f"{name} is on {t.device}, q on {dev}"
+                assert types is None or t.dtype in types, f"{name} must be {types[0]}, not {t.dtype}"
+                assert t.is_contiguous(), f"{name} must be contiguous"
+                assert t.numel() >= count, f"{name} has {t.numel()} elements, {count} are used"
         self.q_scale, self.kv_scale = q_scale, kv_scale
         upr, self.rows = C.mla_decode_geometry(self.s_q, self.h_q, 1, self.topk)
         self.units = self.batch * upr
