@@ -8,9 +8,23 @@ MLA").
 """
 from __future__ import annotations
 
+import functools
+
 import torch
 
 from . import _capi as C
+
+
+def _on_its_device(method):
+    """The library launches on the current device: it is made the runner's own
+    where it is another one."""
+    @functools.wraps(method)
+    def call(self, stream=None):
+        if C._device()[0]() == self.device_index:
+            return method(self, stream)
+        with torch.cuda.device(self.device_index):
+            return method(self, stream)
+    return call
 
 
 class DecodeRunner:
@@ -56,10 +70,11 @@ class DecodeRunner:
                 assert types is None or t.dtype in types, f"{name} must be {types[0]}, not {t.dtype}"
                 assert t.is_contiguous(), f"{name} must be contiguous"
                 assert t.numel() >= count, f"{name} has {t.numel()} elements, {count} are used"
+        self.device_index = dev.index
         self.q_scale, self.kv_scale = q_scale, kv_scale
         upr, self.rows = C.mla_decode_geometry(self.s_q, self.h_q, 1, self.topk)
         self.units = self.batch * upr
-        self.parts = num_sm_parts or C.mla_get_num_sm_parts(dev.index or 0, self.s_q, self.h_q, 1, self.topk)
+        self.parts = num_sm_parts or C.mla_get_num_sm_parts(dev.index, self.s_q, self.h_q, 1, self.topk)
         self.tile_md = torch.empty(self.parts * C.MLA_TILE_MD_INTS, dtype=torch.int32, device=dev)
         self.num_splits = torch.empty(self.units + 1, dtype=torch.int32, device=dev)
         ws_bytes = C.mla_workspace_size(self.batch, self.s_q, self.h_q, 1, self.topk, self.parts)
@@ -80,10 +95,12 @@ class DecodeRunner:
             causal=causal, kv_format=self.kv_format, timeout_ns=timeout_ns, debug_flags=debug_flags,
             sink=sink, d_qk=d_qk, q_scale=q_scale, kv_scale=kv_scale)
 
+    @_on_its_device
     def plan(self, stream=None):
         C.mla_get_metadata(self.cache_seqlens, self.batch, self.s_q, self.h_q, 1, self.topk, self.parts,
                            self.tile_md, self.num_splits, stream)
 
+    @_on_its_device
     def run(self, stream=None):
         if self.topk:
             C.mla_decode_sparse(self.args, self.indices, self.topk, stream)
@@ -91,5 +108,6 @@ class DecodeRunner:
             C.mla_decode_paged(self.args, stream)
         return self.out, self.lse
 
+    @_on_its_device
     def status(self, stream=None):
         return C.mla_query_device_status(self.workspace, stream)
