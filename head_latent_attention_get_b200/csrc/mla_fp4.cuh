@@ -13,7 +13,8 @@
 // two that puts its largest value at 2^11..2^12: what an f16 then cannot hold
 // is below 2^-36 of it, far under the fp32 accumulation. The RoPE part stays
 // bf16 on both sides (times the same power), in MMAs of its own into the same
-// accumulator. Probabilities are f16.
+// accumulator, which RoPE keys up to 2^100 cannot overflow (64 x 2^12 x 2^100).
+// Probabilities are f16.
 //
 // Both operands use one kind of ring entry, 128 tokens x 128 latent dims as two
 // 64-dim slices (32 KB): 64 contiguous code bytes of a token feed an entry, so

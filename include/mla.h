@@ -98,8 +98,9 @@ enum {
    *   [256,288) 32 UE4M3 scales, scale j applies to latent dims [16j, 16j+16)
    *   [288,416) 64 bf16 RoPE dims
    * value = e2m1 * ue4m3 (bit 7 of a scale byte is ignored), used exactly;
-   * the RoPE dims are used as stored. The query is bf16, 576 values. Paged
-   * and token-sparse decoding. */
+   * the RoPE dims are used as stored, up to 2^100 in magnitude (larger ones may
+   * overflow a score). The query is bf16, 576 values. Paged and token-sparse
+   * decoding. */
   MLA_KV_FP4_E2M1 = 3
 };
 
