@@ -55,7 +55,13 @@ __global__ void __launch_bounds__(kCombineThreads) mla_combine_kernel(
         o1[i] = o_u[o_stride + 32 * i];
       }
       float m = -INFINITY;
-      for (int s = 0; s < n; ++s) m = fmaxf(m, lse_u[(size_t)s * rows]);
+      bool nan = false;  // fmaxf passes over NaN
+      for (int s = 0; s < n; ++s) {
+        const float v = lse_u[(size_t)s * rows];
+        nan |= v != v;
+        m = fmaxf(m, v);
+      }
+      if (nan) m = NAN;  // from here on everything is
       if (m != -INFINITY) {
         float sum = 0.f;
         for (int s = 0; s < n; ++s) sum += expf(lse_u[(size_t)s * rows] - m);

@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(fp4::kThreads, 1)
       tc_fence_after();
       if (owner) {
         float inv = 0.f, lse = -INFINITY;
-        if (l_sum > 0.f) {
+        if (!(l_sum <= 0.f)) {  // NaN is no empty row: it goes into both results
           inv = 1.f / l_sum;
           lse = m_used * scale_log2 * 0.693147181f + logf(l_sum * fp4::kProbInv);
         }

@@ -428,7 +428,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
       if (last_gt >= 0 && !pwait_all(pr, &c->o_done[last_gt & 1], (last_gt >> 1) & 1, p)) { stop = true; break; }
       tc_fence_after();
       float inv = 0.f, lse = -INFINITY;
-      if (l_tot > 0.f) {
+      if (!(l_tot <= 0.f)) {  // NaN is no empty row: it goes into both results
         inv = 1.f / l_tot;
         lse = m_used * scale_log2 * 0.693147181f + logf(l_tot * fp4::kProbInv);
       }

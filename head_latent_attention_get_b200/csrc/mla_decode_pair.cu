@@ -661,7 +661,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SPARSE ? kThreadsSpa
       if (last_gt >= 0 && !pwait_all(pr, &c->o_done[last_gt & 1], (last_gt >> 1) & 1, p)) { stop = true; break; }
       tc_fence_after();
       float inv = 0.f, lse = -INFINITY;
-      if (l_tot > 0.f) {
+      if (!(l_tot <= 0.f)) {  // NaN is no empty row: it goes into both results
         inv = 1.f / l_tot;
         lse = m_used * p.scale + logf(l_tot);
       }

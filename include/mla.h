@@ -10,7 +10,7 @@
  * restricted by the causal mask t <= seqlen - s_q + i when `causal` is set,
  * or, for sparse decoding, the token positions listed in `indices[b,i,:]`
  * (entries equal to -1 are ignored). An empty key set gives out = 0 and
- * lse = -inf. Optional: a per-head attention sink (one more logit with a
+ * lse = -inf, a NaN score NaN in both. Optional: a per-head attention sink (one more logit with a
  * zero value, mla_decode_args.sink). With MLA_KV_NVFP4 the rows are 512
  * values that are both K and V (d_qk = d_v = 512) and the query is NVFP4 too.
  *
