@@ -54,7 +54,10 @@ def test_shortest_limit(kv, h_q):
     w = dataclasses.replace(W.get_workload("tiny"), batch=6, s_q=1, h_q=h_q, seqlens=[700 + 37 * i for i in range(6)], causal=False, kv=kv,
                             seed=227)
     inp = W.make_inputs(w, poison_tail=True)
-    out, lse, r = G.run_gpu(inp, dict(timeout_ns=1))
+    for _ in range(3):       # something else may hold the GPU for a millisecond
+        out, lse, r = G.run_gpu(inp, dict(timeout_ns=1))
+        if r.status() == (M.MLA_OK, 0):
+            break
     assert r.status() == (M.MLA_OK, 0)
     G.compare_full(inp, out, lse, kv)
 
