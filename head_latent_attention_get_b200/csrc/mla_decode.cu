@@ -483,6 +483,7 @@ __global__ void __launch_bounds__(MODE == kModeBf16 ? 256 : 256 + 2 * kGatherThr
           const int m = j >> 1, h = j & 1;
           uint8_t* vs = sV + slot * kSlot;
           if (lane == 0 && !timed_wait(c, &c->v_full[slot], (vc / kNV) & 1, p)) stop = true;
+          __syncwarp();  // all lanes write rows of the slot; a shuffle orders no memory
           stop = __shfl_sync(0xffffffffu, stop ? 1 : 0, 0) != 0;
           if (stop) break;
           const int nv_slot = min(64, max(0, nvalid - 64 * h));

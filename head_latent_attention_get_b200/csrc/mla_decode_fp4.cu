@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(fp4::kThreads, 1)
     fp4::load_raw<false>(p, it, rt, sRaw, warp - 8, lane, 0, wait);
   } else if (warp >= 12) {
     fp4::convert_ring<false>(it, rt, sRing, sRaw, c->empty, warp - 12, lane, wait, arrive, [&](int piece) {
-      if (!fp4::wait_warp(&c->q_raw, piece & 1, lane, wait)) return false;
+      if (!fp4::wait_warp(&c->q_raw, piece & 1, wait)) return false;
       fp4::scale_query_rows(sQ, c->q_back[piece & 1], rows_here, warp - 12, lane);
       fence_proxy_async_smem();
       __syncwarp();

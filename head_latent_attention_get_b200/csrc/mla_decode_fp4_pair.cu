@@ -200,7 +200,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
     fp4::load_raw<true>(p, it, rt, sRaw, warp - 8, lane, (int)pr.rank, wait);
   } else if (warp >= 12) {
     fp4::convert_ring<true>(it, rt, sRing, sRaw, c->empty, warp - 12, lane, wait, arrive, [&](int piece) {
-      if (!fp4::wait_warp(&c->q_raw, piece & 1, lane, wait)) return false;
+      if (!fp4::wait_warp(&c->q_raw, piece & 1, wait)) return false;
       fp4::scale_query_rows(sQ, c->q_back[piece & 1], min(64, p.rows - row0), warp - 12, lane);
       fence_proxy_async_smem();
       __syncwarp();
@@ -220,9 +220,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(fp4::kThreads, 1)
           if (i == 4 || (i > 0 && i % 9 == 0)) fence_proxy_async_smem();
           // The rows (acquired from v_loc, fenced by their writers or above) must
           // come before the even CTA's use of them: the count of an asynchronous
-          // store is a release at cluster scope. 64 x 128 x 4096 tokens, us a call:
-          // 137 (134 with a relaxed arrive, which orders nothing; 144 with
-          // arrive.release.cluster, and 147 with that in the converters themselves)
+          // store is a release at cluster scope. 64 x 128 x 4096 tokens, us a call when
+          // it was added: 137 (134 with a relaxed arrive, which orders nothing; 144
+          // with arrive.release.cluster, 147 with that in the converters themselves)
           st_async_u32(map_to_rank(smem_u32(&c->forwarded), 0), 0, map_to_rank(smem_u32(&c->full[sc % kN]), 0));
         }
       }

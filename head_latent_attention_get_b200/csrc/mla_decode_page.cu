@@ -170,6 +170,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool stop = false;
     while (!stop && it.next(pc)) {
       if (lane == 0 && !timed_wait(c, &c->q_empty, (pi & 1) ^ 1, p)) stop = true;
+      __syncwarp();  // all lanes write the query; a shuffle orders no memory
       stop = __shfl_sync(0xffffffffu, stop ? 1 : 0, 0) != 0;
       if (stop) break;
       if (MODE == kModeNvfp4) {

@@ -303,6 +303,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SPARSE ? kThreadsSpa
               uint8_t* dst = sRing + slot * kSlot;
               bool ok = true;
               if (lane == 0) ok = pwait(pr, &c->empty[slot], ((sc / kN) & 1) ^ 1, p);
+              __syncwarp();  // all lanes write the slot; a shuffle orders no memory
               ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
               if (!ok) { stop = true; break; }
               const int x0 = 256 * jd + 128 * (int)pr.rank;
@@ -324,6 +325,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SPARSE ? kThreadsSpa
                     ok = pwait(pr, &c->v_fix, fixc & 1, p);
                   }
                   ++fixc;
+                  __syncwarp();
                   ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
                   if (!ok) { stop = true; break; }
                 }
@@ -388,6 +390,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SPARSE ? kThreadsSpa
             const int slot = sc % kN;
             bool ok = true;
             if (lane == 0) ok = pwait(pr, &c->empty[slot], ((sc / kN) & 1) ^ 1, p);
+            __syncwarp();  // all lanes write the slot; a shuffle orders no memory
             ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
             if (!ok) { stop = true; break; }
             uint8_t* base = sRing + slot * kSlot + (32 * lw) * 128;
@@ -415,6 +418,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SPARSE ? kThreadsSpa
               const int slot = sc % kN;
               bool ok = true;
               if (lane == 0) ok = pwait(pr, &c->empty[slot], ((sc / kN) & 1) ^ 1, p);
+              __syncwarp();  // all lanes write the slot; a shuffle orders no memory
               ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
               if (!ok) { stop = true; break; }
               if (mine) {

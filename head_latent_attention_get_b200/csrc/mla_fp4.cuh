@@ -229,6 +229,7 @@ __device__ __forceinline__ void row_warp(const DecodeParams& p, PieceIter it, Ro
       const int d = gs % kRowDepth;
       bool ok = true;
       if (lane == 0) ok = wait(&rt->empty[d], ((gs / kRowDepth) & 1) ^ 1);
+      __syncwarp();
       ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
       if (!ok) { stop = true; break; }
       const int tok0 = (pc.t0 + (PAIR ? 2 : 1) * g) * kTile, end = min(pc.t1 * kTile, SPARSE ? p.topk : Ls);
@@ -283,13 +284,13 @@ __device__ __forceinline__ void row_warp(const DecodeParams& p, PieceIter it, Ro
   }
 }
 
-// Lane 0 waits for the warp (the first try is made by all lanes).
+// All lanes wait, so that what they read next is ordered for each of them; a shuffle
+// of one lane's outcome orders no memory. Decode and combine, us, 64 x 128 x 4096 /
+// 64 x 64 x 8192 / ragged 16 heads / 32 x 128 topk 2048: 121 / 172 / 376 / 49; one
+// lane waiting, with a warp barrier 131 / 177 / 372 / 50, without it 131 / 173 / 367 / 50.
 template <class Wait>
-__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int lane, Wait wait) {
-  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-  bool ok = true;
-  if (lane == 0) ok = wait(bar, parity);
-  return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, Wait wait) {
+  return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || __all_sync(0xffffffffu, wait(bar, parity));
 }
 
 // Entry e of a phase. K, and a single CTA's V: latent dims 128 e .. of the
@@ -317,11 +318,11 @@ __device__ __forceinline__ void load_raw(const DecodeParams& p, const PieceIter&
   while (!stop && ph.next()) {
     const bool k = ph.is_k();
     const int step = ph.step(), d = step % kRowDepth;
-    if (k && !wait_warp(&rt->full[d], (step / kRowDepth) & 1, lane, wait)) break;
+    if (k && !wait_warp(&rt->full[d], (step / kRowDepth) & 1, wait)) break;
 #pragma unroll 1
     for (int e = 0; e < 4; ++e, ++n) {
       const int r = n % kRaw;
-      if (!wait_warp(&rt->raw_empty[r], ((n / kRaw) & 1) ^ 1, lane, wait)) { stop = true; break; }
+      if (!wait_warp(&rt->raw_empty[r], ((n / kRaw) & 1) ^ 1, wait)) { stop = true; break; }
       const int32_t* rows = rt->row[d] + entry_token<PAIR>(k, e, rank) + 32 * w;
       const int d0 = entry_dim<PAIR>(k, e, rank);
       uint8_t* buf = raw + r * kRawBytes;
@@ -368,7 +369,7 @@ __device__ __forceinline__ void load_rope(const DecodeParams& p, const PieceIter
     pos.advance(4);
     if (!ph.is_k()) continue;
     const int step = ph.step(), d = step % kRowDepth;
-    if (!wait_warp(&rt->full[d], (step / kRowDepth) & 1, lane, wait)) break;
+    if (!wait_warp(&rt->full[d], (step / kRowDepth) & 1, wait)) break;
     // rows first: nothing but the copies is left to do once the place is free
     const int32_t* rows = rt->row[d] + entry_token<PAIR>(true, 0, rank) + (lane >> 3);
     int row[32];
@@ -376,7 +377,7 @@ __device__ __forceinline__ void load_rope(const DecodeParams& p, const PieceIter
     for (int i = 0; i < 32; ++i) row[i] = rows[4 * i];
     __syncwarp();
     if (lane == 0) mbar_arrive(&rt->empty[d]);
-    if (!wait_warp(free, step & 1, lane, wait)) break;
+    if (!wait_warp(free, step & 1, wait)) break;
 #pragma unroll
     for (int i = 0; i < 32; ++i)
       cp_async16(sw128(ring + pos.slot * kSlot, 4 * i + (lane >> 3), lane & 7),
@@ -419,7 +420,7 @@ __device__ __forceinline__ void convert_ring(const PieceIter& it, RowTable* rt, 
 #pragma unroll 1
     for (int e = grp; e < 4; e += 2, ++use) {
       const RingPos at = pos.at(e);
-      if (!wait_warp(&rt->raw_full[grp], use & 1, lane, wait)) { stop = true; break; }
+      if (!wait_warp(&rt->raw_full[grp], use & 1, wait)) { stop = true; break; }
       uint4 codes[4];
       uint32_t sc[4];
 #pragma unroll
@@ -429,7 +430,7 @@ __device__ __forceinline__ void convert_ring(const PieceIter& it, RowTable* rt, 
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&rt->raw_empty[grp]);
-      if (!wait_warp(&empty[at.slot], at.parity ^ 1u, lane, wait)) { stop = true; break; }
+      if (!wait_warp(&empty[at.slot], at.parity ^ 1u, wait)) { stop = true; break; }
       uint8_t* s = ring + at.slot * kSlot + (q >> 1) * kSlice;
 #pragma unroll
       for (int j = 0; j < 4; ++j) store_item(codes[j], sc[j], s, tok + 8 * j, 4 * (q & 1));
