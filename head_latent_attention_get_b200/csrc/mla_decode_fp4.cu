@@ -458,8 +458,8 @@ cudaError_t launch_decode_fp4(const CUtensorMap& tq, const DecodeParams& p, int 
   // <= 16 rows run in the 32-row kernel: what the extra rows hold (P^T rows and
   // O^T columns of their own) is never stored. The rule is the row count: O's MMAs,
   // rescale and epilogue grow with NR. 48 rows in the 48-row kernel against the
-  // 64-row one, us a step: 64 requests x 8192 tokens 181 / 188, x 40 rows x 4096
-  // 108 / 110; 32 rows (ragged, 128 requests) in the 32-row kernel 403 / 409
+  // 64-row one, us a step: 64 requests x 8192 tokens 182 / 184, x 40 rows x 4096
+  // 108 / 109; 32 rows (ragged, 128 requests) in the 32-row kernel 410 / 412
   if (p.rows <= 32) return sparse ? launch_one<32, true>(tq, p, parts, stream) : launch_one<32, false>(tq, p, parts, stream);
   if (p.rows <= 48) return sparse ? launch_one<48, true>(tq, p, parts, stream) : launch_one<48, false>(tq, p, parts, stream);
   return sparse ? launch_one<64, true>(tq, p, parts, stream) : launch_one<64, false>(tq, p, parts, stream);
